@@ -66,7 +66,15 @@ KERNEL_SOURCE = {"absmean_kernel": "bl_weights.cu", "ternarize_flat_kernel": "bl
                  "t5_to_i2_kernel": "bl_gemm_sm100.cu", "splitk_reduce_kernel": "bl_gemm_sm100.cu",
                  "pack_kernel": "bl_weights.cu",
                  "backward_dx_tile_kernel": "bl_backward.cu", "backward_dx_reduce_kernel": "bl_backward.cu",
-                 "backward_dw_kernel": "bl_backward.cu", "backward_dw1_kernel": "bl_backward.cu"}
+                 "backward_dw_kernel": "bl_backward.cu", "backward_dw1_kernel": "bl_backward.cu",
+                 "act_grad_kernel": "bl_act_grad.cu", "column_sum_kernel": "bl_act_grad.cu",
+                 "gemm_grad_kernel": "bl_gemm_grad.cu", "grad_parts_kernel": "bl_gemm_grad.cu",
+                 "i2_to_bf16_kernel": "bl_gemm_grad.cu", "pad_rows_kernel": "bl_gemm_grad.cu",
+                 "grad_rowmax_kernel": "bl_gemm_grad.cu", "grad_rowscale_kernel": "bl_gemm_grad.cu",
+                 "grad_split_kernel": "bl_gemm_grad.cu", "i8_to_f16_kernel": "bl_gemm_grad.cu",
+                 "residual_norm_kernel": "bl_norm.cu", "residual_norm_long_kernel": "bl_norm.cu",
+                 "residual_norm_grad_kernel": "bl_norm.cu", "residual_norm_grad_stats_kernel": "bl_norm.cu",
+                 "residual_norm_grad_cols_kernel": "bl_norm.cu", "residual_norm_grad_sum_kernel": "bl_norm.cu"}
 
 
 def csrc_digest(kernel: str | None = None) -> str:
@@ -957,6 +965,10 @@ PROFILE_CASES = {
     "pack_3b_up": dict(N=8640, K=3200, fmt=0, M=1, sigma=0.02, op="pack"),
     "actquant_16x40000": dict(N=16, K=40000, fmt=0, M=16, sigma=0.02, op="actquant"),
     "quantize_3b_up_t5": dict(N=8640, K=3200, fmt=1, M=1, sigma=0.02, op="quantize"),
+    "train_3b_up": dict(N=8640, K=3200, fmt=0, M=4096, sigma=0.02, op="train"),
+    "train_3b_odd_m130": dict(N=3201, K=3200, fmt=0, M=130, sigma=0.02, op="train"),
+    "norm_3b": dict(N=64, K=3200, fmt=0, M=4096, sigma=0.02, op="norm"),
+    "norm_70b_down": dict(N=64, K=28672, fmt=0, M=512, sigma=0.01, op="norm"),
 }
 
 
@@ -1023,6 +1035,40 @@ def run_profile_case(name):
             B.bitlinear_backward_dx(packed, fmt, gamma, N, K, dy, dx, bws)
             B.bitlinear_backward_dw(dy, xq, sc, gamma, dw)
         status.append(B.bitlinear_device_status(bws))
+    if c["op"] == "train":  # the epilogue product and its gradients
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        y, z = (torch.empty((M, N), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        bias = torch.randn(N, generator=g, device=dev) * 0.2
+        dy = (torch.randn(M, N, generator=g, device=dev) * 1e-3).to(torch.bfloat16)
+        dz, dbias = torch.empty_like(dy), torch.empty(N, device=dev)
+        dx, dw = torch.empty((M, K), dtype=torch.bfloat16, device=dev), torch.empty((N, K), device=dev)
+        xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+        B.bitlinear_quantize_acts(x, xq, scale)
+        need = max(B.bitlinear_forward_epilogue_workspace_bytes(M, N, K, fmt, B.BL_BF16),
+                   B.bitlinear_epilogue_backward_workspace_bytes(M, N),
+                   B.bitlinear_backward_dx_bf16_workspace_bytes(M, N, K, fmt),
+                   B.bitlinear_backward_dw_bf16_workspace_bytes(M, N, K))
+        tws = torch.zeros(need, dtype=torch.uint8, device=dev)
+        for _ in range(3):
+            B.bitlinear_forward_epilogue(packed, fmt, gamma, N, K, x, scale, y, tws, bias=bias, act=B.BL_ACT_SILU,
+                                         preact=z)
+            B.bitlinear_epilogue_backward(dy, z, B.BL_ACT_SILU, dz, dbias, tws)
+            B.bitlinear_backward_dx_bf16(packed, fmt, gamma, N, K, dz, dx, tws)
+            B.bitlinear_backward_dw_bf16(dz, xq, scale, gamma, dw, tws)
+        status.append(B.bitlinear_device_status(tws))
+    if c["op"] == "norm":  # the norms around a block and their gradients
+        r, dy, dh = (torch.randn(M, K, generator=g, device=dev).to(torch.bfloat16) for _ in range(3))
+        h, dr, db = (torch.empty_like(x) for _ in range(3))
+        w1, w2, gate = (1 + 0.1 * torch.randn(K, generator=g, device=dev) for _ in range(3))
+        dw1, dw2, dgate = (torch.empty(K, device=dev) for _ in range(3))
+        xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+        sc = torch.empty(M, dtype=torch.float32, device=dev)
+        nws = torch.zeros(B.bitlinear_residual_norm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
+        kw = dict(post=B.BL_NORM_RMS, post_w=w1, gate=gate, pre=B.BL_NORM_RMS, pre_w=w2)
+        for _ in range(3):
+            B.bitlinear_residual_norm(x, r, h, xq=xq, scale=sc, **kw)
+            B.bitlinear_residual_norm_backward(dy, dh, x, h, dr, db, nws, dpost_w=dw1, dgate=dgate, dpre_w=dw2, **kw)
+        status.append(B.bitlinear_device_status(nws))
     torch.cuda.synchronize()
     print(json.dumps({"profile_case": name, **c, "status": status}))
     if any(status):

@@ -21,6 +21,8 @@ BL_ERR_WORKSPACE_TOO_SMALL, BL_ERR_CUDA, BL_ERR_DEVICE_TIMEOUT, BL_ERR_BAD_CODE 
 BL_ERR_SCRATCH_LIMIT = 8
 BL_F32, BL_BF16, BL_I8, BL_I32 = 0, 1, 2, 3
 BL_PACK_I2, BL_PACK_T5, BL_PACK_B1 = 0, 1, 2
+BL_ACT_NONE, BL_ACT_RELU, BL_ACT_RELU2, BL_ACT_SILU, BL_ACT_GELU = 0, 1, 2, 3, 4
+BL_NORM_NONE, BL_NORM_RMS, BL_NORM_LAYER = 0, 1, 2
 BL_WS_HEADER_BYTES = 256
 
 # (name, restype, argtypes) of every exported entry point
@@ -45,11 +47,34 @@ SIGNATURES = {
     "bitlinear_backward_dx_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
     "bitlinear_backward_dx": (_I, [_P, _I, _P, _I64, _I64, _P, _I, _I64, _P, _P, _SZ, _P]),
     "bitlinear_backward_dw": (_I, [_P, _I, _P, _P, _P, _I64, _I64, _I64, _P, _P]),
+    "bitlinear_forward_epilogue_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "bitlinear_forward_epilogue": (_I, [_P, _I, _P, _I64, _I64, _P, _I, _P, _I64, _P, _I, _P, _P, _P, _I, _P, _SZ, _P]),
+    "bitlinear_epilogue_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "bitlinear_epilogue_backward": (_I, [_P, _I, _P, _I, _I, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "bitlinear_backward_dx_bf16_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
+    "bitlinear_backward_dx_bf16": (_I, [_P, _I, _P, _I64, _I64, _P, _I64, _P, _I, _P, _SZ, _P]),
+    "bitlinear_backward_dw_bf16_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "bitlinear_backward_dw_bf16": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P]),
+    "bitlinear_residual_norm": (_I, [_P, _P, _I, _P, _I, _I64, _I64, _P, _P, _I, _P, _P, _P]),
+    "bitlinear_residual_norm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "bitlinear_residual_norm_backward": (_I, [_P, _P, _I, _P, _P, _I, _P, _I, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
     "bitlinear_selftest_wait_timeout": (_I, [_P, _SZ, _P]),
     "bitlinear_device_status": (_I, [_P, _P]),
     "bitlinear_status_string": (C.c_char_p, [_I]),
     "bitlinear_version": (_I, []),
 }
+
+
+class ResidualNormParams(C.Structure):
+    """bl_residual_norm_params"""
+    _fields_ = [("post", _I), ("post_eps", _F), ("post_w", _P), ("post_b", _P), ("gate", _P), ("gate_rows", _I64),
+                ("res_scale", _F), ("branch_scale", _F), ("pre", _I), ("pre_eps", _F), ("pre_w", _P), ("pre_b", _P)]
+
+
+class ResidualNormGrads(C.Structure):
+    """bl_residual_norm_grads"""
+    _fields_ = [("dpost_w", _P), ("dpost_b", _P), ("dgate", _P), ("dpre_w", _P), ("dpre_b", _P)]
+
 
 _lib = None
 _lock = threading.Lock()
@@ -249,6 +274,209 @@ def bitlinear_backward_dw(dy, xq, scale, gamma, dw, stream=None) -> None:
     _check(lib().bitlinear_backward_dw(_ptr(dy), dtype_code(dy), _ptr(xq), _ptr(scale), _ptr(gamma), M, N, K,
                                        _ptr(dw), _stream(stream)),
            "bitlinear_backward_dw")
+
+
+# --- the product with its epilogue, its gradients, the norms around a block -------
+#
+# These calls check shapes, dtypes, contiguity and that every tensor is on one
+# CUDA device, and run on that device (the current stream there unless one is
+# given); the current device of the caller does not change.
+
+_F32, _BF16, _INT8, _U8 = torch.float32, torch.bfloat16, torch.int8, torch.uint8
+_FLOATS = (_F32, _BF16)
+
+
+def _want(name, t, shape, dtypes, dev):
+    """t is None or a contiguous tensor of this shape and one of the dtypes on dev."""
+    if t is None:
+        return
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _matrix(name, t):
+    """The device of a 2-D CUDA tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _workspace(ws, dev):
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, stream, *args):
+    """lib().name(*args, stream) on dev."""
+    fn = getattr(_lib or lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = torch.cuda.current_stream() if stream is None else stream
+        status = fn(*args, st.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = torch.cuda.current_stream() if stream is None else stream
+            status = fn(*args, st.cuda_stream)
+    if status != BL_OK:
+        raise BitLinearError(status, name)
+
+
+def bitlinear_forward_epilogue_workspace_bytes(M: int, N: int, K: int, fmt: int, xdt: int) -> int:
+    return int(lib().bitlinear_forward_epilogue_workspace_bytes(M, N, K, fmt, xdt))
+
+
+def bitlinear_forward_epilogue(packed, fmt, gamma, N, K, x, scale, y, ws, bias=None, act=BL_ACT_NONE, residual=None,
+                               preact=None, stream=None) -> None:
+    """y = act(x W_q^T dequantized + bias) + residual; preact receives the argument of act."""
+    dev = _matrix("x", x)
+    M = x.shape[0]
+    _want("x", x, (M, K), (_F32, _BF16, _INT8), dev)
+    _want("packed", packed, (N, bitlinear_packed_row_bytes(K, fmt)), (_U8,), dev)
+    _want("gamma", gamma, (1,), (_F32,), dev)
+    _want("scale", scale, (M,), (_F32,), dev)
+    _want("y", y, (M, N), _FLOATS, dev)
+    _want("bias", bias, (N,), (_F32,), dev)
+    _want("residual", residual, (M, N), (y.dtype,), dev)
+    _want("preact", preact, (M, N), (y.dtype,), dev)
+    wp, wn = _workspace(ws, dev)
+    _call("bitlinear_forward_epilogue", dev, stream, packed.data_ptr(), fmt, gamma.data_ptr(), N, K, x.data_ptr(),
+          _DT[x.dtype], scale.data_ptr(), M, _raw(bias), act, _raw(residual), _raw(preact), y.data_ptr(), _DT[y.dtype],
+          wp, wn)
+
+
+def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
+    return int(lib().bitlinear_epilogue_backward_workspace_bytes(M, N))
+
+
+def bitlinear_epilogue_backward(dy, z, act, dz, dbias, ws, stream=None) -> None:
+    """dz = dy act'(z) and dbias = its column sums (either may be None)."""
+    dev = _matrix("dy", dy)
+    M, N = dy.shape
+    _want("dy", dy, (M, N), _FLOATS, dev)
+    _want("z", z, (M, N), _FLOATS, dev)
+    _want("dz", dz, (M, N), (dy.dtype,), dev)
+    _want("dbias", dbias, (N,), (_F32,), dev)
+    wp, wn = _workspace(ws, dev)
+    _call("bitlinear_epilogue_backward", dev, stream, dy.data_ptr(), _DT[dy.dtype], _raw(z),
+          BL_F32 if z is None else _DT[z.dtype], act, M, N, _raw(dz), _raw(dbias), wp, wn)
+
+
+def bitlinear_backward_dx_bf16_workspace_bytes(M: int, N: int, K: int, fmt: int) -> int:
+    return int(lib().bitlinear_backward_dx_bf16_workspace_bytes(M, N, K, fmt))
+
+
+def bitlinear_backward_dx_bf16(packed, fmt, gamma, N, K, dz, dx, ws, stream=None) -> None:
+    """dx = gamma dz W_q on the tensor cores (bf16 dz, dx bf16 or fp32)."""
+    dev = _matrix("dz", dz)
+    M = dz.shape[0]
+    _want("dz", dz, (M, N), (_BF16,), dev)
+    _want("packed", packed, (N, bitlinear_packed_row_bytes(K, fmt)), (_U8,), dev)
+    _want("gamma", gamma, (1,), (_F32,), dev)
+    _want("dx", dx, (M, K), _FLOATS, dev)
+    wp, wn = _workspace(ws, dev)
+    _call("bitlinear_backward_dx_bf16", dev, stream, packed.data_ptr(), fmt, gamma.data_ptr(), N, K, dz.data_ptr(), M,
+          dx.data_ptr(), _DT[dx.dtype], wp, wn)
+
+
+def bitlinear_backward_dw_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().bitlinear_backward_dw_bf16_workspace_bytes(M, N, K))
+
+
+def bitlinear_backward_dw_bf16(dz, xq, scale, gamma, dw, ws, stream=None) -> None:
+    """dW = gamma dz^T x_deq on the tensor cores (bf16 dz, fp32 dW)."""
+    dev = _matrix("dz", dz)
+    M, N = dz.shape
+    K = xq.shape[-1]
+    _want("dz", dz, (M, N), (_BF16,), dev)
+    _want("xq", xq, (M, K), (_INT8,), dev)
+    _want("scale", scale, (M,), (_F32,), dev)
+    _want("gamma", gamma, (1,), (_F32,), dev)
+    _want("dw", dw, (N, K), (_F32,), dev)
+    wp, wn = _workspace(ws, dev)
+    _call("bitlinear_backward_dw_bf16", dev, stream, dz.data_ptr(), xq.data_ptr(), scale.data_ptr(), gamma.data_ptr(),
+          M, N, K, dw.data_ptr(), wp, wn)
+
+
+def _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
+                 pre_b, pre_eps):
+    if gate is not None and gate_rows < 1:
+        gate_rows = max(M, 1)       # one row for every token
+    for name, t in (("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w), ("pre_b", pre_b)):
+        _want(name, t, (K,), (_F32,), dev)
+    if gate is not None:
+        rows = -(-M // gate_rows)
+        if gate.dim() == 1:
+            _want("gate", gate, (K,), (_F32,), dev)
+            if rows > 1:
+                raise ValueError(f"gate: one row, expected {rows}")
+        else:
+            _want("gate", gate, (rows, K), (_F32,), dev)
+    return ResidualNormParams(post, post_eps, _raw(post_w), _raw(post_b), _raw(gate), gate_rows if gate is not None else 0,
+                              res_scale, branch_scale, pre, pre_eps, _raw(pre_w), _raw(pre_b))
+
+
+def bitlinear_residual_norm(b, r, h, post=BL_NORM_NONE, post_w=None, post_b=None, post_eps=1e-5, gate=None,
+                            gate_rows=0, res_scale=1.0, branch_scale=1.0, pre=BL_NORM_RMS, pre_w=None, pre_b=None,
+                            pre_eps=1e-5, y=None, xq=None, scale=None, stream=None) -> None:
+    """h = res_scale r + branch_scale gate norm_post(b); y = norm_pre(h); xq, scale its INT8 codes.
+
+    gate: [rows, K] with one row for every gate_rows tokens (0: one row for all, also as [K])."""
+    dev = _matrix("b", b)
+    M, K = b.shape
+    _want("b", b, (M, K), _FLOATS, dev)
+    _want("r", r, (M, K), _FLOATS, dev)
+    _want("h", h, (M, K), (r.dtype,), dev)
+    _want("y", y, (M, K), _FLOATS, dev)
+    _want("xq", xq, (M, K), (_INT8,), dev)
+    _want("scale", scale, (M,), (_F32,), dev)
+    p = _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
+                     pre_b, pre_eps)
+    _call("bitlinear_residual_norm", dev, stream, C.addressof(p), b.data_ptr(), _DT[b.dtype], r.data_ptr(),
+          _DT[r.dtype], M, K, _raw(h), _raw(y), BL_F32 if y is None else _DT[y.dtype], _raw(xq), _raw(scale))
+
+
+def bitlinear_residual_norm_backward_workspace_bytes(M: int, K: int, gate_rows: int = 0) -> int:
+    """gate_rows as for the call; 0 without a gate or with one row for every token."""
+    return int(lib().bitlinear_residual_norm_backward_workspace_bytes(M, K, gate_rows if gate_rows > 0 else max(M, 1)))
+
+
+def bitlinear_residual_norm_backward(dy, dh, b, h, dr, db, ws, post=BL_NORM_NONE, post_w=None, post_b=None,
+                                     post_eps=1e-5, gate=None, gate_rows=0, res_scale=1.0, branch_scale=1.0,
+                                     pre=BL_NORM_RMS, pre_w=None, pre_eps=1e-5, dpost_w=None, dpost_b=None, dgate=None,
+                                     dpre_w=None, dpre_b=None, stream=None) -> None:
+    """Gradients of bitlinear_residual_norm from dy (of y) and dh (of h, or None)."""
+    dev = _matrix("dy", dy)
+    M, K = dy.shape
+    _want("dy", dy, (M, K), _FLOATS, dev)
+    _want("b", b, (M, K), _FLOATS, dev)
+    _want("h", h, (M, K), _FLOATS, dev)
+    _want("dh", dh, (M, K), (h.dtype,), dev)
+    _want("dr", dr, (M, K), (h.dtype,), dev)
+    _want("db", db, (M, K), (b.dtype,), dev)
+    for name, t in (("dpost_w", dpost_w), ("dpost_b", dpost_b), ("dpre_w", dpre_w), ("dpre_b", dpre_b)):
+        _want(name, t, (K,), (_F32,), dev)
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        _want("dgate", dgate, tuple(gate.shape), (_F32,), dev)
+    p = _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
+                     None, pre_eps)
+    g = ResidualNormGrads(_raw(dpost_w), _raw(dpost_b), _raw(dgate), _raw(dpre_w), _raw(dpre_b))
+    wp, wn = _workspace(ws, dev)
+    _call("bitlinear_residual_norm_backward", dev, stream, C.addressof(p), dy.data_ptr(), _DT[dy.dtype], _raw(dh),
+          b.data_ptr(), _DT[b.dtype], h.data_ptr(), _DT[h.dtype], M, K, _raw(dr), _raw(db), C.addressof(g), wp, wn)
 
 
 def bitlinear_device_status(ws, stream=None) -> int:

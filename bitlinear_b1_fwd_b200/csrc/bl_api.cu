@@ -23,6 +23,9 @@ inline bool float_dt(int dt) { return dt == BL_F32 || dt == BL_BF16; }
 inline bool fmt_ok(int fmt) { return fmt == BL_PACK_I2 || fmt == BL_PACK_T5 || fmt == BL_PACK_B1; }
 inline bool tern_fmt_ok(int fmt) { return fmt == BL_PACK_I2 || fmt == BL_PACK_T5; }  // ternary formats
 
+inline bool act_ok(int act) { return act >= BL_ACT_NONE && act <= BL_ACT_GELU; }
+inline bool norm_ok(int kind) { return kind >= BL_NORM_NONE && kind <= BL_NORM_LAYER; }
+
 inline bl_status cuda_status(cudaError_t e) { return e == cudaSuccess ? BL_OK : BL_ERR_CUDA; }
 
 bool nk_ok(int64_t N, int64_t K) {
@@ -185,9 +188,9 @@ bl_status bitlinear_layernorm_quantize_acts(const void* x, int xdt, const float*
   return cuda_status(bl::launch_ln_quant(x, xdt, ln_w, ln_b, eps, M, K, y, xq, scale, static_cast<cudaStream_t>(stream)));
 }
 
-bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
-                            const void* x, int xdt, float* scale, int64_t M, void* y, int ydt, void* ws,
-                            size_t ws_bytes, void* stream) {
+static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K, const void* x,
+                              int xdt, float* scale, int64_t M, void* y, int ydt, const bl::Epilogue& ep, void* ws,
+                              size_t ws_bytes, void* stream) {
   if (!fmt_ok(fmt) || !(float_dt(xdt) || xdt == BL_I8) || !(float_dt(ydt) || ydt == BL_I32))
     return BL_ERR_INVALID_VALUE;
   if (!m_ok(M) || !nk_ok(N, K)) return BL_ERR_INVALID_VALUE;
@@ -210,7 +213,7 @@ bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, 
       fmt = BL_PACK_I2;
     }
     if (bl::gemv_max_tokens(fmt, bitlinear_packed_row_bytes(K, fmt)) < 1) return BL_ERR_UNSUPPORTED;
-    return cuda_status(bl::launch_gemv(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::one_group(N), ws, st));
+    return cuda_status(bl::launch_gemv(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::one_group(N, ep), ws, st));
   }
   uint8_t* scratch = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
   const int8_t* xq = static_cast<const int8_t*>(x);
@@ -231,7 +234,28 @@ bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, 
     scratch += round256(static_cast<size_t>(N * rb2));
   }
   int32_t* part = bl::gemm_split_k(M, N, K) > 1 ? reinterpret_cast<int32_t*>(scratch) : nullptr;
-  return cuda_status(bl::launch_gemm_i2(xq, w2, rb2, gamma, scale, y, ydt, M, N, K, N, part, ws, 0, 0, st));
+  return cuda_status(bl::launch_gemm_i2(xq, w2, rb2, gamma, scale, y, ydt, M, N, K, N, part, ws, 0, 0, st, ep));
+}
+
+bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
+                            const void* x, int xdt, float* scale, int64_t M, void* y, int ydt, void* ws,
+                            size_t ws_bytes, void* stream) {
+  return forward_with(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::no_epilogue(), ws, ws_bytes, stream);
+}
+
+size_t bitlinear_forward_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
+  return bitlinear_forward_workspace_bytes(M, N, K, fmt, xdt);
+}
+
+bl_status bitlinear_forward_epilogue(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
+                                     const void* x, int xdt, float* scale, int64_t M, const float* bias, int act,
+                                     const void* residual, void* preact, void* y, int ydt, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  if (!float_dt(ydt) || !act_ok(act)) return BL_ERR_INVALID_VALUE;
+  if (preact != nullptr && (preact == y || preact == residual)) return BL_ERR_INVALID_VALUE;
+  if (!aligned(bias, 4) || !aligned(residual, 16) || !aligned(preact, 16)) return BL_ERR_MISALIGNED;
+  return forward_with(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::Epilogue{bias, residual, preact, act}, ws,
+                      ws_bytes, stream);
 }
 
 // Several weight matrices sharing one token batch (for example a block's Q, K
@@ -298,6 +322,7 @@ bl_status bitlinear_forward_grouped(const uint8_t* packed, int fmt, const float*
     if (bl::gemv_max_tokens(fmt, bitlinear_packed_row_bytes(K, fmt)) < 1) return BL_ERR_UNSUPPORTED;
     bl::RowGroups rg{};
     rg.n = static_cast<int>(ngroups);
+    rg.ep = bl::no_epilogue();
     int64_t end = 0;
     for (int64_t g = 0; g < ngroups; ++g) rg.end[g] = (end += group_rows[g]);
     return cuda_status(bl::launch_gemv(packed, fmt, gammas, N, K, x, xdt, scale, M, y, ydt, rg, ws, st));
@@ -377,6 +402,206 @@ bl_status bitlinear_backward_dw(const void* dy, int dydt, const int8_t* xq, cons
   if (!aligned(dy, 16) || !aligned(xq, 16) || !aligned(dw, 16) || !aligned(scale, 4) || !aligned(gamma, 4))
     return BL_ERR_MISALIGNED;
   return cuda_status(bl::launch_backward_dw(dy, dydt, xq, scale, gamma, M, N, K, dw, static_cast<cudaStream_t>(stream)));
+}
+
+// Gradients through the epilogue of bitlinear_forward_epilogue.
+size_t bitlinear_epilogue_backward_workspace_bytes(int64_t M, int64_t N) {
+  if (!m_ok(M) || N < 1 || N > kMaxRows) return 0;
+  return BL_WS_HEADER_BYTES + round256(static_cast<size_t>(bl::act_grad_row_blocks(M, N)) * N * sizeof(float));
+}
+
+bl_status bitlinear_epilogue_backward(const void* dy, int dydt, const void* z, int zdt, int act, int64_t M, int64_t N,
+                                      void* dz, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  if (!float_dt(dydt) || !float_dt(zdt) || !act_ok(act) || !m_ok(M) || N < 1 || N > kMaxRows)
+    return BL_ERR_INVALID_VALUE;
+  if (!aligned(dbias, 4)) return BL_ERR_MISALIGNED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) return dbias == nullptr ? BL_OK : cuda_status(cudaMemsetAsync(dbias, 0, N * sizeof(float), st));
+  if (dz == nullptr && dbias == nullptr) return BL_ERR_INVALID_VALUE;
+  if (dy == nullptr || (act != BL_ACT_NONE && z == nullptr) || ws == nullptr) return BL_ERR_INVALID_VALUE;
+  if (z != nullptr && dz == z) return BL_ERR_INVALID_VALUE;
+  if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16) || !aligned(ws, 16)) return BL_ERR_MISALIGNED;
+  if (ws_bytes < bitlinear_epilogue_backward_workspace_bytes(M, N)) return BL_ERR_WORKSPACE_TOO_SMALL;
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES);
+  return cuda_status(bl::launch_act_grad(dy, dydt, z, zdt, act, M, N, dz, dbias, part, st));
+}
+
+// The gradient products on the tensor cores.
+size_t bitlinear_backward_dx_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt) {
+  if (N < 1 || !m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
+  const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
+  size_t bytes = BL_WS_HEADER_BYTES + round256(static_cast<size_t>(N) * bl::grad_ld(K) * 2);
+  if (fmt != BL_PACK_I2) bytes += round256(static_cast<size_t>(N) * rb2);
+  if (N % 8 != 0) bytes += round256(static_cast<size_t>(M) * bl::grad_ld(N) * 2);
+  const int ks = bl::grad_dx_parts(M, N, K);
+  if (ks > 1) bytes += round256(static_cast<size_t>(ks) * M * K * sizeof(float));
+  return bytes;
+}
+
+bl_status bitlinear_backward_dx_bf16(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
+                                     const void* dz, int64_t M, void* dx, int dxdt, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  if (!fmt_ok(fmt) || !float_dt(dxdt) || !m_ok(M) || N < 1 || !nk_ok(N, K)) return BL_ERR_INVALID_VALUE;
+  if (M == 0) return BL_OK;
+  if (packed == nullptr || gamma == nullptr || dz == nullptr || dx == nullptr || ws == nullptr)
+    return BL_ERR_INVALID_VALUE;
+  if (!aligned(packed, 16) || !aligned(dz, 16) || !aligned(dx, 16) || !aligned(gamma, 4) || !aligned(ws, 16))
+    return BL_ERR_MISALIGNED;
+  if (ws_bytes < bitlinear_backward_dx_bf16_workspace_bytes(M, N, K, fmt)) return BL_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* scratch = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
+  const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
+  const uint8_t* w2 = packed;
+  if (fmt != BL_PACK_I2) {
+    const int64_t rb = bitlinear_packed_row_bytes(K, fmt);
+    const cudaError_t e = fmt == BL_PACK_T5 ? bl::launch_t5_to_i2(packed, N, K, rb, scratch, rb2, st)
+                                            : bl::launch_b1_to_i2(packed, N, K, rb, scratch, rb2, st);
+    if (e != cudaSuccess) return BL_ERR_CUDA;
+    w2 = scratch;
+    scratch += round256(static_cast<size_t>(N) * rb2);
+  }
+  const int64_t ldw = bl::grad_ld(K);
+  uint16_t* w16 = reinterpret_cast<uint16_t*>(scratch);
+  if (bl::launch_i2_to_bf16(w2, N, rb2, w16, st) != cudaSuccess) return BL_ERR_CUDA;
+  scratch += round256(static_cast<size_t>(N) * ldw * 2);
+  const uint16_t* g = static_cast<const uint16_t*>(dz);
+  int64_t ldg = N;
+  if (N % 8 != 0) {  // TMA rows are multiples of 16 bytes
+    ldg = bl::grad_ld(N);
+    uint16_t* padded = reinterpret_cast<uint16_t*>(scratch);
+    if (bl::launch_pad_rows(g, M, N, ldg, padded, st) != cudaSuccess) return BL_ERR_CUDA;
+    g = padded;
+    scratch += round256(static_cast<size_t>(M) * ldg * 2);
+  }
+  return cuda_status(bl::launch_grad_dx(g, ldg, w16, ldw, gamma, M, N, K, dx, dxdt, reinterpret_cast<float*>(scratch),
+                                        ws, st));
+}
+
+size_t bitlinear_backward_dw_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (N < 1 || !m_ok(M) || !nk_ok(N, K)) return 0;
+  return BL_WS_HEADER_BYTES + round256(static_cast<size_t>(bl::grad_rowmax_ranges(M)) * N * 4) +
+         2 * round256(static_cast<size_t>(N) * 4) + 2 * round256(static_cast<size_t>(M) * bl::grad_ld(N) * 2) +
+         round256(static_cast<size_t>(M) * bl::grad_ld(K) * 2);
+}
+
+bl_status bitlinear_backward_dw_bf16(const void* dz, const int8_t* xq, const float* scale, const float* gamma,
+                                     int64_t M, int64_t N, int64_t K, float* dw, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  if (!m_ok(M) || N < 1 || !nk_ok(N, K) || dw == nullptr) return BL_ERR_INVALID_VALUE;
+  if (!aligned(dw, 16)) return BL_ERR_MISALIGNED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) return cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(N) * K * sizeof(float), st));
+  if (dz == nullptr || xq == nullptr || scale == nullptr || gamma == nullptr || ws == nullptr)
+    return BL_ERR_INVALID_VALUE;
+  if (!aligned(dz, 16) || !aligned(xq, 16) || !aligned(scale, 4) || !aligned(gamma, 4) || !aligned(ws, 16))
+    return BL_ERR_MISALIGNED;
+  if (ws_bytes < bitlinear_backward_dw_bf16_workspace_bytes(M, N, K)) return BL_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* p = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
+  auto take = [&p](size_t bytes) {
+    uint8_t* q = p;
+    p += round256(bytes);
+    return q;
+  };
+  bl::GradDwScratch s;
+  s.maxes = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(bl::grad_rowmax_ranges(M)) * N * 4));
+  s.rowscale = reinterpret_cast<float*>(take(static_cast<size_t>(N) * 4));
+  s.rowinv = reinterpret_cast<float*>(take(static_cast<size_t>(N) * 4));
+  s.hi = take(static_cast<size_t>(M) * bl::grad_ld(N) * 2);
+  s.lo = take(static_cast<size_t>(M) * bl::grad_ld(N) * 2);
+  s.x = take(static_cast<size_t>(M) * bl::grad_ld(K) * 2);
+  return cuda_status(bl::launch_grad_dw(static_cast<const uint16_t*>(dz), xq, scale, gamma, M, N, K, dw, s, ws, st));
+}
+
+// The norms around a block's end.
+static bl_status residual_norm_params_ok(const bl_residual_norm_params* p) {
+  if (p == nullptr || !norm_ok(p->post) || !norm_ok(p->pre)) return BL_ERR_INVALID_VALUE;
+  if (p->post != BL_NORM_NONE && (!(p->post_eps > 0.0f) || !std::isfinite(p->post_eps))) return BL_ERR_INVALID_VALUE;
+  if (p->pre != BL_NORM_NONE && (!(p->pre_eps > 0.0f) || !std::isfinite(p->pre_eps))) return BL_ERR_INVALID_VALUE;
+  if (!std::isfinite(p->res_scale) || !std::isfinite(p->branch_scale)) return BL_ERR_INVALID_VALUE;
+  if (p->gate != nullptr && p->gate_rows < 1) return BL_ERR_INVALID_VALUE;
+  if (!aligned(p->post_w, 4) || !aligned(p->post_b, 4) || !aligned(p->gate, 4) || !aligned(p->pre_w, 4) ||
+      !aligned(p->pre_b, 4))
+    return BL_ERR_MISALIGNED;
+  return BL_OK;
+}
+// gate rows past the last token are not looked at: counts beyond M act as M
+static bl_residual_norm_params clamp_gate(const bl_residual_norm_params& p, int64_t M) {
+  bl_residual_norm_params q = p;
+  if (q.gate == nullptr || q.gate_rows > M) q.gate_rows = M;
+  return q;
+}
+
+bl_status bitlinear_residual_norm(const bl_residual_norm_params* p, const void* b, int bdt, const void* r, int rdt,
+                                  int64_t M, int64_t K, void* h, void* y, int ydt, int8_t* xq, float* scale,
+                                  void* stream) {
+  if (!float_dt(bdt) || !float_dt(rdt) || (y != nullptr && !float_dt(ydt)) || !m_ok(M) || K < 1 || K > kMaxK)
+    return BL_ERR_INVALID_VALUE;
+  const bl_status ps = residual_norm_params_ok(p);
+  if (ps != BL_OK) return ps;
+  if (M == 0) return BL_OK;
+  if ((h == nullptr && y == nullptr && xq == nullptr) || (xq == nullptr) != (scale == nullptr))
+    return BL_ERR_INVALID_VALUE;
+  if (b == nullptr || r == nullptr || y == b || y == r || (y != nullptr && y == h) || h == b)
+    return BL_ERR_INVALID_VALUE;
+  if (!aligned(b, 16) || !aligned(r, 16) || !aligned(h, 16) || !aligned(y, 16) || !aligned(xq, 16) ||
+      !aligned(scale, 4))
+    return BL_ERR_MISALIGNED;
+  return cuda_status(bl::launch_residual_norm(clamp_gate(*p, M), b, bdt, r, rdt, M, K, h, y, ydt, xq, scale,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+size_t bitlinear_residual_norm_backward_workspace_bytes(int64_t M, int64_t K, int64_t gate_rows) {
+  if (!m_ok(M) || K < 1 || K > kMaxK || gate_rows < 0) return 0;
+  if (M == 0) return BL_WS_HEADER_BYTES;
+  const int64_t blocks = bl::norm_grad_blocks(M);
+  const int64_t per = gate_rows > M ? M : gate_rows;
+  const int64_t gates = per > 0 ? blocks + (M + per - 1) / per : 0;
+  return BL_WS_HEADER_BYTES + round256(static_cast<size_t>(blocks) * 4 * K * sizeof(float)) +
+         round256(static_cast<size_t>(gates) * K * sizeof(float)) + round256(static_cast<size_t>(M) * 8 * sizeof(float));
+}
+
+bl_status bitlinear_residual_norm_backward(const bl_residual_norm_params* p, const void* dy, int dydt, const void* dh,
+                                           const void* b, int bdt, const void* h, int rdt, int64_t M, int64_t K,
+                                           void* dr, void* db, const bl_residual_norm_grads* g, void* ws,
+                                           size_t ws_bytes, void* stream) {
+  if (!float_dt(dydt) || !float_dt(bdt) || !float_dt(rdt) || !m_ok(M) || K < 1 || K > kMaxK || g == nullptr)
+    return BL_ERR_INVALID_VALUE;
+  const bl_status ps = residual_norm_params_ok(p);
+  if (ps != BL_OK) return ps;
+  if (g->dgate != nullptr && p->gate == nullptr) return BL_ERR_INVALID_VALUE;
+  if (!aligned(g->dpost_w, 4) || !aligned(g->dpost_b, 4) || !aligned(g->dgate, 4) || !aligned(g->dpre_w, 4) ||
+      !aligned(g->dpre_b, 4))
+    return BL_ERR_MISALIGNED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    float* const sums[4] = {g->dpost_w, g->dpost_b, g->dpre_w, g->dpre_b};  // a gate of no tokens has no rows
+    for (float* s : sums)
+      if (s != nullptr && cudaMemsetAsync(s, 0, K * sizeof(float), st) != cudaSuccess) return BL_ERR_CUDA;
+    return BL_OK;
+  }
+  if (dr == nullptr && db == nullptr && g->dpost_w == nullptr && g->dpost_b == nullptr && g->dgate == nullptr &&
+      g->dpre_w == nullptr && g->dpre_b == nullptr)
+    return BL_ERR_INVALID_VALUE;
+  if (dy == nullptr || b == nullptr || h == nullptr || ws == nullptr) return BL_ERR_INVALID_VALUE;
+  // in place: dr over dh, and db over dy of the same type; an output over anything else is refused
+  if (dr != nullptr && (dr == dy || dr == b || dr == h || dr == db)) return BL_ERR_INVALID_VALUE;
+  if (db != nullptr && (db == dh || db == b || db == h || (db == dy && bdt != dydt))) return BL_ERR_INVALID_VALUE;
+  if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(b, 16) || !aligned(h, 16) || !aligned(dr, 16) ||
+      !aligned(db, 16) || !aligned(ws, 16))
+    return BL_ERR_MISALIGNED;
+  const int64_t gate_rows = p->gate != nullptr ? (p->gate_rows > M ? M : p->gate_rows) : 0;
+  const size_t need = bitlinear_residual_norm_backward_workspace_bytes(M, K, gate_rows);
+  if (ws_bytes < need) return BL_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t blocks = bl::norm_grad_blocks(M);
+  const int64_t gates = gate_rows > 0 ? blocks + (M + gate_rows - 1) / gate_rows : 0;
+  uint8_t* s = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
+  float* part = reinterpret_cast<float*>(s);
+  s += round256(static_cast<size_t>(blocks) * 4 * K * sizeof(float));
+  float* gpart = reinterpret_cast<float*>(s);
+  s += round256(static_cast<size_t>(gates) * K * sizeof(float));
+  return cuda_status(bl::launch_residual_norm_grad(clamp_gate(*p, M), dy, dydt, dh, b, bdt, h, rdt, M, K, dr, db,
+                                                   g->dpost_w, g->dpost_b, g->dgate, g->dpre_w, g->dpre_b, part, gpart,
+                                                   s, st));
 }
 
 bl_status bitlinear_selftest_wait_timeout(void* ws, size_t ws_bytes, void* stream) {

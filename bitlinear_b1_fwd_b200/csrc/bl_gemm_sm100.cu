@@ -28,8 +28,10 @@
 #include <cstring>
 
 #include "bl_common.cuh"
+#include "bl_epilogue.cuh"
 #include "bl_kernels.h"
 #include "bl_sm100.cuh"
+#include "bl_tensormap.h"
 
 namespace bl {
 namespace {
@@ -179,7 +181,8 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
     gemm_i2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, int y_tma, const float* __restrict__ gamma,
                    const float* __restrict__ scale, void* __restrict__ y, int ydt, int M, int N, int K, int ldy, int ks,
-                   int32_t* __restrict__ part, WsHeader* __restrict__ hdr, long long limit, int skip_producer) {
+                   int32_t* __restrict__ part, WsHeader* __restrict__ hdr, long long limit, int skip_producer,
+                   const Epilogue ep_arg) {
   pdl_enter(gamma, scale, y, part, hdr);
   using Cfg = GemmCfg<BT>;
   constexpr int SX = Cfg::kSX, SP = Cfg::kSP, SB = Cfg::kSB;
@@ -390,11 +393,13 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
     const uint32_t esz = (ydt == BL_BF16) ? 2u : 4u;
     const bool use_tma = y_tma != 0 && ks == 1;
     const float g = __ldcg(gamma);
+    const Epilogue ep = epilogue_after_wait(ep_arg);
     int tc = 0, chunk = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++tc) {
       const Unit w = unit_of(u);
       const int a = tc & 1;
       const int n = w.n_t * kBN + 32 * q + lane;
+      const float bias = (ep.bias != nullptr && n < N) ? __ldcg(ep.bias + n) : 0.0f;
       // dequant factor c_t = (gamma s_t) / 127 of each token of the tile, once
       float* cf = cfac + a * BT;
       if (ks == 1)
@@ -424,6 +429,9 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
         tmem_load<Cfg::kChunk>(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * BT + j0),
                                acc);
         const int t0 = w.t_t * BT + j0;
+        if (ks == 1 && ydt != BL_I32)
+          epilogue_chunk<Cfg::kChunk>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy,
+                                      n < N ? M - t0 : 0);
         if (ks > 1) {
           if (n < N) {
 #pragma unroll
@@ -443,7 +451,7 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
             if (ydt == BL_I32) {
               *reinterpret_cast<int32_t*>(col + j * 128 * 4) = v;
             } else {
-              const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
+              const float yv = __uint_as_float(acc[j]);
               if (ydt == BL_F32)
                 *reinterpret_cast<float*>(col + j * 128 * 4) = yv;
               else
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
               if (ydt == BL_I32) {
                 static_cast<int32_t*>(y)[o] = v;
               } else {
-                const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
+                const float yv = __uint_as_float(acc[j]);
                 if (ydt == BL_F32)
                   static_cast<float*>(y)[o] = yv;
                 else
@@ -495,24 +503,18 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
 // Four consecutive outputs per thread when N % 4 == 0.
 __global__ void __launch_bounds__(256)
     splitk_reduce_kernel(const int32_t* __restrict__ part, int ks, int M, int N, int ldy, const float* __restrict__ gamma,
-                         const float* __restrict__ scale, void* __restrict__ y, int ydt) {
+                         const float* __restrict__ scale, void* __restrict__ y, int ydt, const Epilogue ep_arg) {
   pdl_enter(part, gamma, scale, y);
+  const Epilogue ep = epilogue_after_wait(ep_arg);
   __shared__ float sh_g;  // gamma once per CTA
   if (threadIdx.x == 0) sh_g = __ldcg(gamma);
   __syncthreads();
   const float g = sh_g;
   const int64_t plane = static_cast<int64_t>(M) * N;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  auto emit = [&](int64_t o, int t, int v) {
-    if (ydt == BL_I32) {
-      static_cast<int32_t*>(y)[o] = v;
-    } else {
-      const float yv = __fmul_rn(__int2float_rn(v), dequant_factor(g, __ldcg(scale + t)));
-      if (ydt == BL_F32)
-        static_cast<float*>(y)[o] = yv;
-      else
-        static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(yv);
-    }
+  auto emit = [&](int t, int64_t n, int v) {  // row stride ldy
+    const float cf = ydt == BL_I32 ? 0.0f : dequant_factor(g, __ldcg(scale + t));
+    epilogue_store(ep, y, ydt, static_cast<int64_t>(t) * ldy + n, n, v, cf);
   };
   if ((N % 4) == 0) {
     const int64_t n4 = plane / 4;
@@ -527,18 +529,18 @@ __global__ void __launch_bounds__(256)
       }
       const int64_t o = 4 * i;
       const int t = static_cast<int>(o / N);
-      const int64_t yo = static_cast<int64_t>(t) * ldy + (o - static_cast<int64_t>(t) * N);  // row stride ldy
-      emit(yo, t, s.x);
-      emit(yo + 1, t, s.y);
-      emit(yo + 2, t, s.z);
-      emit(yo + 3, t, s.w);
+      const int64_t n = o - static_cast<int64_t>(t) * N;
+      emit(t, n, s.x);
+      emit(t, n + 1, s.y);
+      emit(t, n + 2, s.z);
+      emit(t, n + 3, s.w);
     }
   } else {
     for (int64_t o = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; o < plane; o += stride) {
       int s = __ldcg(part + o);
       for (int kz = 1; kz < ks; ++kz) s += __ldcg(part + kz * plane + o);
       const int t = static_cast<int>(o / N);
-      emit(static_cast<int64_t>(t) * ldy + (o - static_cast<int64_t>(t) * N), t, s);
+      emit(t, o - static_cast<int64_t>(t) * N, s);
     }
   }
 }
@@ -593,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_i2_2sm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_y, int y_tma, const float* __restrict__ gamma,
                        const float* __restrict__ scale, void* __restrict__ y, int ydt, int M, int N, int K, int ldy,
-                       WsHeader* __restrict__ hdr, long long limit) {
+                       WsHeader* __restrict__ hdr, long long limit, const Epilogue ep_arg) {
   pdl_enter(gamma, scale, y, hdr);
   using Cfg = Gemm2Cfg<BT>;
   extern __shared__ uint8_t smem_raw[];
@@ -757,12 +759,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3, et = threadIdx.x - 256;
     const uint32_t esz = (ydt == BL_BF16) ? 2u : 4u;
     const float g = __ldcg(gamma);
+    const Epilogue ep = epilogue_after_wait(ep_arg);
     int tc = 0, chunk = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++tc) {
       const int a = tc & 1;
       const int n_t = tile % n_tiles, t_t = tile / n_tiles;
       const int nbase = n_t * 2 * kBN + static_cast<int>(rank) * kBN;
       const int n = nbase + 32 * q + lane;
+      const float bias = (ep.bias != nullptr && n < N) ? __ldcg(ep.bias + n) : 0.0f;
       float* cf = cfac + a * BT;
       for (int j = et; j < BT; j += 128) {
         const int t = t_t * BT + j;
@@ -788,6 +792,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         uint32_t acc[32];
         tmem_load<32>(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * BT + j0), acc);
         const int t0 = t_t * BT + j0;
+        if (ydt != BL_I32)
+          epilogue_chunk<32>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy, n < N ? M - t0 : 0);
         if (y_tma) {
           uint8_t* sb = ystage + (chunk & 1) * kYStage;
           if (chunk >= 2) {  // the store issued from this buffer two chunks ago has read it
@@ -801,7 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             if (ydt == BL_I32) {
               *reinterpret_cast<int32_t*>(col + j * 128 * 4) = v;
             } else {
-              const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
+              const float yv = __uint_as_float(acc[j]);
               if (ydt == BL_F32)
                 *reinterpret_cast<float*>(col + j * 128 * 4) = yv;
               else
@@ -824,7 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
               if (ydt == BL_I32) {
                 static_cast<int32_t*>(y)[o] = v;
               } else {
-                const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
+                const float yv = __uint_as_float(acc[j]);
                 if (ydt == BL_F32)
                   static_cast<float*>(y)[o] = yv;
                 else
@@ -950,22 +956,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- host side --------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (fn == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 bool encode_2d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stride,
                   uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
   EncodeTiledFn fn = encode_fn();
@@ -1001,7 +991,7 @@ bool encode_y(CUtensorMap* m, void* y, int ydt, int64_t M, int64_t N, int64_t ld
 template <int BT>
 cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int ks, int32_t* part, void* ws,
-                           long long limit, int skip_producer, cudaStream_t st) {
+                           long long limit, int skip_producer, cudaStream_t st, const Epilogue& ep) {
   CUtensorMap tx, tw;
   if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K), 128, BT,
                     CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1021,14 +1011,14 @@ cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   e = launch_pdl(kern, grid, GemmCfg<BT>::kThreads, smem, st, tx, tw, ty, y_tma, gamma, scale, y, ydt, static_cast<int>(M),
                  static_cast<int>(N), static_cast<int>(K), static_cast<int>(ldy), ks, part, static_cast<WsHeader*>(ws), limit,
-                 skip_producer);
+                 skip_producer, ep);
   if (e != cudaSuccess) return e;
   if (ks > 1) {
     const int64_t work = (N % 4 == 0) ? M * N / 4 : M * N;
     int64_t rgrid = (work + 255) / 256;
     if (rgrid > 8 * sms) rgrid = 8 * sms;
     e = launch_pdl(splitk_reduce_kernel, static_cast<unsigned>(rgrid), 256, 0, st, static_cast<const int32_t*>(part),
-                   ks, static_cast<int>(M), static_cast<int>(N), static_cast<int>(ldy), gamma, scale, y, ydt);
+                   ks, static_cast<int>(M), static_cast<int>(N), static_cast<int>(ldy), gamma, scale, y, ydt, ep);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
@@ -1037,7 +1027,7 @@ cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const
 template <int BT>
 cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                             void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, void* ws, long long limit,
-                            cudaStream_t st) {
+                            cudaStream_t st, const Epilogue& ep) {
   CUtensorMap tx, tw;
   if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K), 128,
                     BT / 2, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1059,7 +1049,7 @@ cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, cons
                                                                      static_cast<int>(M), static_cast<int>(N),
                                                                      static_cast<int>(K), static_cast<int>(ldy),
                                                                      static_cast<WsHeader*>(ws),
-                                                                     limit); if (le_ != cudaSuccess) return le_; }
+                                                                     limit, ep); if (le_ != cudaSuccess) return le_; }
   return cudaGetLastError();
 }
 
@@ -1097,16 +1087,16 @@ int gemm_split_k(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int32_t* part, void* ws,
-                           long long limit_cycles, int skip_producer, cudaStream_t st) {
+                           long long limit_cycles, int skip_producer, cudaStream_t st, const Epilogue& ep) {
   const long long limit = limit_cycles > 0 ? limit_cycles : kTimeoutCycles;
   if (M > 128 && !skip_producer)
-    return launch_gemm_2sm<256>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ws, limit, st);
+    return launch_gemm_2sm<256>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ws, limit, st, ep);
   const int ks = (part != nullptr && !skip_producer) ? gemm_split_k(M, N, K) : 1;
   switch (gemm_token_tile(M)) {
-    case 16: return launch_gemm_bt<16>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
-    case 32: return launch_gemm_bt<32>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
-    case 64: return launch_gemm_bt<64>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
-    default: return launch_gemm_bt<128>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
+    case 16: return launch_gemm_bt<16>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
+    case 32: return launch_gemm_bt<32>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
+    case 64: return launch_gemm_bt<64>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
+    default: return launch_gemm_bt<128>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
   }
 }
 

@@ -16,6 +16,7 @@
 // sums meet by warp reduction; the dequantization y = acc * (gamma s / 127)
 // ("§5.3") is fused into the store.
 #include "bl_common.cuh"
+#include "bl_epilogue.cuh"
 #include "bl_gemv.cuh"
 #include "bl_kernels.h"
 
@@ -380,6 +381,7 @@ quant_act_fast_n<8>(e, s_tok[m], c127, q);
       consume(bufB);
     }
     __syncthreads();  // every part of every row of the tile has been added
+    const Epilogue ep = epilogue_after_wait(rg.ep);
     for (int r = threadIdx.x; r < static_cast<int>(nr); r += blockDim.x) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -387,12 +389,7 @@ quant_act_fast_n<8>(e, s_tok[m], c127, q);
         racc[m * kGemvTileRows + r] = 0;
         const int64_t o = m * N + row0 + t0 + r;
         const float cf = rg.n == 1 ? cfac[m] : dequant_factor(sh_gam[row_group(rg, row0 + t0 + r)], s_tok[m]);
-        if (ydt == BL_I32)
-          static_cast<int32_t*>(y)[o] = a;
-        else if (ydt == BL_F32)
-          static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
-        else
-          static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+        epilogue_store(ep, y, ydt, o, row0 + t0 + r, a, cf);
       }
     }
     __syncthreads();  // the row sums are zero again for the next tile
@@ -843,6 +840,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       }
     }
     __syncthreads();  // every part of every row of the tile has been added
+    const Epilogue ep = epilogue_after_wait(rg.ep);
     for (int r = threadIdx.x; r < static_cast<int>(nr); r += blockDim.x) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -850,12 +848,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         racc[m * kGemvTileRows + r] = 0;
         const int64_t o = m * N + row0 + t0 + r;
         const float cf = rg.n == 1 ? cfac[m] : dequant_factor(sh_gam[row_group(rg, row0 + t0 + r)], s_tok[m]);
-        if (ydt == BL_I32)
-          static_cast<int32_t*>(y)[o] = a;
-        else if (ydt == BL_F32)
-          static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
-        else
-          static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+        epilogue_store(ep, y, ydt, o, row0 + t0 + r, a, cf);
       }
     }
     __syncthreads();  // the row sums are zero again for the next tile
@@ -1075,18 +1068,14 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     }
   }
   __syncthreads();  // every part of every row has been added
+  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = threadIdx.x; r < nrows; r += nthr) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int a = racc[m * kGemvTileRows + r] - corr[m];
       const int64_t o = m * N + row0 + r;
       const float cf = rg.n == 1 ? cfac[m] : dequant_factor(sh_gam[row_group(rg, row0 + r)], s_tok[m]);
-      if (ydt == BL_I32)
-        static_cast<int32_t*>(y)[o] = a;
-      else if (ydt == BL_F32)
-        static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
-      else
-        static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+      epilogue_store(ep, y, ydt, o, row0 + r, a, cf);
     }
   }
 }
@@ -1317,16 +1306,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     }
   }
   __syncthreads();  // every part of every row has been added
+  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = threadIdx.x; r < nrows; r += nthr) {
     const int a = racc[r] - corr;
     const int64_t o = row0 + r;
     const float cf = rg.n == 1 ? cfac : dequant_factor(sh_gam[row_group(rg, o)], s_tok);
-    if (ydt == BL_I32)
-      static_cast<int32_t*>(y)[o] = a;
-    else if (ydt == BL_F32)
-      static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
-    else
-      static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+    epilogue_store(ep, y, ydt, o, o, a, cf);
   }
 }
 
@@ -1474,7 +1459,7 @@ static cudaError_t launch_gemv_mt(int mt, const uint8_t* packed, int64_t rowbyte
 // Runs the GEMV over all M tokens in groups that fit in shared memory.
 cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
                         const void* x, int xdt, float* scale, int64_t M, void* y, int ydt,
-                        const RowGroups& rg, void* ws, cudaStream_t st) {
+                        const RowGroups& rg_all, void* ws, cudaStream_t st) {
   const int per = (fmt == BL_PACK_I2) ? 4 : (fmt == BL_PACK_T5 ? 5 : 8);
   const int64_t rowbytes = ((K + per - 1) / per + 15) / 16 * 16;
   const int mt_max = gemv_max_tokens(fmt, rowbytes);
@@ -1486,11 +1471,11 @@ cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int6
   const bool lean = (fmt == BL_PACK_I2 && rowbytes <= 2 * kI2Plane) || (fmt == BL_PACK_B1 && rowbytes <= kI2Plane);
   if (fmt == BL_PACK_B1 && !lean) return cudaErrorInvalidValue;
   if (fmt == BL_PACK_I2 && M == 1 && gemv1_fits(N, K, rowbytes, xdt))
-    return launch_gemv1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
+    return launch_gemv1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg_all, ws, st);
   if (fmt == BL_PACK_T5 && M == 1 && gemv1_t5_fits(N, K, rowbytes, xdt))
-    return launch_gemv1_t5(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
+    return launch_gemv1_t5(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg_all, ws, st);
   if (fmt == BL_PACK_B1 && M == 1 && gemv1_b1_fits(N, K, rowbytes, xdt))
-    return launch_gemv1_b1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
+    return launch_gemv1_b1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg_all, ws, st);
   const int esz = (xdt == BL_F32) ? 4 : (xdt == BL_BF16 ? 2 : 1);
   const int ysz = (ydt == BL_BF16) ? 2 : 4;
   for (int64_t m0 = 0; m0 < M; m0 += mt_max) {
@@ -1498,6 +1483,9 @@ cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int6
     const void* xm = static_cast<const uint8_t*>(x) + m0 * K * esz;
     float* sm = scale + m0;
     void* ym = static_cast<uint8_t*>(y) + m0 * N * ysz;
+    RowGroups rg = rg_all;  // the residual and the kept pre-activation start at these tokens too
+    if (rg.ep.res != nullptr) rg.ep.res = static_cast<const uint8_t*>(rg.ep.res) + m0 * N * ysz;
+    if (rg.ep.pre != nullptr) rg.ep.pre = static_cast<uint8_t*>(rg.ep.pre) + m0 * N * ysz;
     cudaError_t e;
     if (fmt == BL_PACK_I2 && mt >= 2 && mt <= 4 && gemv_mt_fits(rowbytes, N, mt)) {
       if (xdt == BL_F32) e = launch_gemv_mt_cs_n<BL_F32>(mt, packed, rowbytes, gamma, N, K, xm, sm, ym, ydt, 1, rg, st);

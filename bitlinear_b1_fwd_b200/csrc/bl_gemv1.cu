@@ -30,6 +30,7 @@
 // previous kernel writes).  After the wait it reads the token, quantizes it
 // and streams its rows with D 16-byte loads in flight per thread.
 #include "bl_common.cuh"
+#include "bl_epilogue.cuh"
 #include "bl_gemv.cuh"
 #include "bl_kernels.h"
 #include "bl_sm100.cuh"
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
 
   // 6. dequantize and store the CTA's outputs (coalesced)
   const float cf1 = dequant_factor(sh_gam[0], s);
+  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = tid; r < nrows; r += T) {
     const int a = rsum[r];
     const int64_t n = row0 + r;
@@ -411,12 +413,7 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
       while (gi + 1 < rg.n && n >= sh_end[gi]) ++gi;
       cf = dequant_factor(sh_gam[gi], s);
     }
-    if (ydt == BL_I32)
-      static_cast<int32_t*>(y)[n] = a;
-    else if (ydt == BL_F32)
-      static_cast<float*>(y)[n] = __fmul_rn(__int2float_rn(a), cf);
-    else
-      static_cast<__nv_bfloat16*>(y)[n] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+    epilogue_store(ep, y, ydt, n, n, a, cf);
   }
   if (XDT != BL_I8 && write_scale && b == 0 && tid == 0) scale[0] = s;
 }
@@ -714,6 +711,7 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
 
   // 6. dequantize and store the CTA's outputs (coalesced)
   const float cf1 = dequant_factor(sh_gam[0], s);
+  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = tid; r < nrows; r += T) {
     const int a = rsum[r];
     const int64_t n = row0 + r;
@@ -723,12 +721,7 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
       while (gi + 1 < rg.n && n >= sh_end[gi]) ++gi;
       cf = dequant_factor(sh_gam[gi], s);
     }
-    if (ydt == BL_I32)
-      static_cast<int32_t*>(y)[n] = a;
-    else if (ydt == BL_F32)
-      static_cast<float*>(y)[n] = __fmul_rn(__int2float_rn(a), cf);
-    else
-      static_cast<__nv_bfloat16*>(y)[n] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+    epilogue_store(ep, y, ydt, n, n, a, cf);
   }
   if (XDT != BL_I8 && write_scale && b == 0 && tid == 0) scale[0] = s;
 }
@@ -993,6 +986,7 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
 
   // 6. dequantize and store the CTA's outputs (coalesced)
   const float cf1 = dequant_factor(sh_gam[0], s);
+  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = tid; r < nrows; r += T) {
     const int a = rsum[r];
     const int64_t n = row0 + r;
@@ -1002,12 +996,7 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
       while (gi + 1 < rg.n && n >= sh_end[gi]) ++gi;
       cf = dequant_factor(sh_gam[gi], s);
     }
-    if (ydt == BL_I32)
-      static_cast<int32_t*>(y)[n] = a;
-    else if (ydt == BL_F32)
-      static_cast<float*>(y)[n] = __fmul_rn(__int2float_rn(a), cf);
-    else
-      static_cast<__nv_bfloat16*>(y)[n] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
+    epilogue_store(ep, y, ydt, n, n, a, cf);
   }
   if (XDT != BL_I8 && write_scale && b == 0 && tid == 0) scale[0] = s;
 }

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "bitlinear.h"
+
 namespace bl {
 
 // Launch with programmatic stream serialization (see pdl_enter): the kernel
@@ -27,6 +29,16 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 // absmean: the last CTA folds 2^lgR chunk sums per lane (lgR <= 11 allows
 // 2^19 chunks of 8192 elements, so N*K <= 2^32).
 constexpr int kFinishMaxLevels = 11;
+
+// What follows the dequantization of an output: bias [N], act (bl_act; negative:
+// nothing follows), residual and kept pre-activation [M, N] of y's type.
+struct Epilogue {
+  const float* bias;
+  const void* res;
+  void* pre;
+  int act;
+};
+inline Epilogue no_epilogue() { return Epilogue{nullptr, nullptr, nullptr, -1}; }
 
 // Number of SMs of the current device (cached per device).
 constexpr int kMaxDevices = 64;
@@ -64,26 +76,30 @@ int gemm_token_tile(int64_t M);
 // nullptr to keep every tile whole.
 cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int32_t* part, void* ws,
-                           long long limit_cycles, int skip_producer, cudaStream_t st);
+                           long long limit_cycles, int skip_producer, cudaStream_t st,
+                           const Epilogue& ep = no_epilogue());  // with an epilogue ldy == N
 int gemm_split_k(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_t5_to_i2(const uint8_t* t5, int64_t N, int64_t K, int64_t rb5, uint8_t* i2, int64_t rb2,
                             cudaStream_t st);
 // Output rows in up to kMaxRowGroups consecutive groups, each with its own
-// gamma (row n belongs to the first group g with n < end[g]).
+// gamma (row n belongs to the first group g with n < end[g]), and what follows
+// their dequantization.
 constexpr int kMaxRowGroups = 8;
 struct RowGroups {
   int n;
   int64_t end[kMaxRowGroups];
+  Epilogue ep;
 };
 __host__ __device__ inline int row_group(const RowGroups& rg, int64_t row) {
   int g = 0;
   while (g + 1 < rg.n && row >= rg.end[g]) ++g;
   return g;
 }
-inline RowGroups one_group(int64_t N) {
+inline RowGroups one_group(int64_t N, const Epilogue& ep = no_epilogue()) {
   RowGroups rg{};
   rg.n = 1;
   rg.end[0] = N;
+  rg.ep = ep;
   return rg;
 }
 
@@ -95,6 +111,44 @@ cudaError_t launch_backward_dx(const uint8_t* packed, int64_t rowbytes, const fl
                                const void* dy, int dydt, int64_t M, float* dx, double* part, cudaStream_t st);
 cudaError_t launch_backward_dw(const void* dy, int dydt, const int8_t* xq, const float* scale, const float* gamma,
                                int64_t M, int64_t N, int64_t K, float* dw, cudaStream_t st);
+
+// Gradients through the forward's epilogue; part: act_grad_row_blocks(M, N)
+// rows of N fp32 partial sums (dbias without them when there is one block).
+int64_t act_grad_row_blocks(int64_t M, int64_t N);
+cudaError_t launch_act_grad(const void* dy, int dydt, const void* z, int zdt, int act, int64_t M, int64_t N, void* dz,
+                            float* dbias, float* part, cudaStream_t st);
+
+// The gradient products on the tensor cores.  grad_ld: row stride (elements)
+// of a scratch array of n columns.  dx: dz bf16 with row stride lddz (a
+// multiple of 8), w the codes in bf16 with row stride ldw; part: ks M K fp32
+// where ks = grad_dx_parts(M, N, K) > 1.
+int64_t grad_ld(int64_t n);
+int grad_dx_parts(int64_t M, int64_t N, int64_t K);
+int64_t grad_rowmax_ranges(int64_t M);
+cudaError_t launch_i2_to_bf16(const uint8_t* i2, int64_t N, int64_t rowbytes, uint16_t* w, cudaStream_t st);
+cudaError_t launch_pad_rows(const uint16_t* src, int64_t M, int64_t N, int64_t ld, uint16_t* dst, cudaStream_t st);
+cudaError_t launch_grad_dx(const uint16_t* dz, int64_t lddz, const uint16_t* w, int64_t ldw, const float* gamma,
+                           int64_t M, int64_t N, int64_t K, void* dx, int dxdt, float* part, void* ws,
+                           cudaStream_t st);
+struct GradDwScratch {
+  uint32_t* maxes;           // [grad_rowmax_ranges(M)][N]
+  float *rowscale, *rowinv;  // [N]
+  void *hi, *lo;             // fp16 [M][grad_ld(N)]
+  void* x;                   // fp16 [M][grad_ld(K)]
+};
+cudaError_t launch_grad_dw(const uint16_t* dz, const int8_t* xq, const float* scale, const float* gamma, int64_t M,
+                           int64_t N, int64_t K, float* dw, const GradDwScratch& s, void* ws, cudaStream_t st);
+
+// The norms around a block's end.  Backward scratch: part [norm_grad_blocks(M)]
+// [4][K], gpart [norm_grad_blocks(M) + gate rows][K], stats [M][8] fp32.
+using NormParams = bl_residual_norm_params;
+cudaError_t launch_residual_norm(const NormParams& p, const void* b, int bdt, const void* r, int rdt, int64_t M,
+                                 int64_t K, void* h, void* y, int ydt, int8_t* xq, float* scale, cudaStream_t st);
+int64_t norm_grad_blocks(int64_t M);
+cudaError_t launch_residual_norm_grad(const NormParams& p, const void* dy, int dydt, const void* dh, const void* b,
+                                      int bdt, const void* h, int rdt, int64_t M, int64_t K, void* dr, void* db,
+                                      float* dw1, float* db1, float* dgate, float* dw2, float* db2, float* part,
+                                      float* gpart, void* stats, cudaStream_t st);
 
 // One-token 2-bit GEMV (column-stationary, early start): K % 16 == 0, rows of
 // at most 8192 bytes, and fp32 tokens only when K is small enough for the raw

@@ -292,6 +292,126 @@ BL_API bl_status bitlinear_backward_dw(const void *dy, int dydt, const int8_t *x
                                     const float *gamma, int64_t M, int64_t N, int64_t K, float *dw,
                                     void *stream);
 
+/* BitLinear forward with bias, activation and residual in its epilogue:
+ *   z[m, n] = fl(fl(acc[m, n] c_m) + bias[n]),  c_m = (gamma s_m) / 127,
+ *   y[m, n] = act(z[m, n]) + residual[m, n]     (fp32, one rounding to ydt),
+ * with acc and c_m as in bitlinear_forward.  z does not depend on M or on the
+ * kernel that serves the sizes (acc is an exact integer, c_m z two fp32
+ * roundings): a token gives the same y alone and in a batch.
+ *   packed, fmt, gamma, x, xdt, scale  as for bitlinear_forward.
+ *   bias      [N] fp32, or NULL (0).
+ *   act       bl_act; BL_ACT_GELU is z Phi(z) with the error function.
+ *   residual  [M, N] of type ydt, or NULL (0); may be y itself (in place).
+ *   preact    [M, N] of type ydt: receives z for the backward pass, or NULL;
+ *             must not overlap y or residual.
+ *   y         [M, N] BL_F32 or BL_BF16.
+ *   ws        at least bitlinear_forward_epilogue_workspace_bytes(...). */
+typedef enum {
+  BL_ACT_NONE = 0,
+  BL_ACT_RELU = 1,
+  BL_ACT_RELU2 = 2, /* max(z, 0)^2 */
+  BL_ACT_SILU = 3,  /* z / (1 + exp(-z)) */
+  BL_ACT_GELU = 4   /* z (1 + erf(z / sqrt 2)) / 2 */
+} bl_act;
+BL_API size_t bitlinear_forward_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt);
+BL_API bl_status bitlinear_forward_epilogue(const uint8_t *packed, int fmt, const float *gamma, int64_t N, int64_t K,
+                                         const void *x, int xdt, float *scale, int64_t M, const float *bias, int act,
+                                         const void *residual, void *preact, void *y, int ydt, void *ws,
+                                         size_t ws_bytes, void *stream);
+
+/* Gradients through that epilogue: for an upstream gradient dy of y and the
+ * kept z,
+ *   dz[m, n] = dy[m, n] act'(z[m, n])      (fp32, one rounding to the type),
+ *   dbias[n] = sum_m dz[m, n]              (of the unrounded fp32 products,
+ *              fp32 sums in a fixed order: the same bits on every call);
+ * the residual's gradient is dy itself.  act' is 0 where z = 0 for the two
+ * ReLUs; with BL_ACT_NONE z may be NULL.
+ *   dy, dz [M, N] of type dydt (dz may be dy, or NULL);  z [M, N] of type zdt.
+ *   dbias  [N] fp32, or NULL (not both NULL); zeros when M is 0.
+ *   ws     at least bitlinear_epilogue_backward_workspace_bytes(M, N). */
+BL_API size_t bitlinear_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
+BL_API bl_status bitlinear_epilogue_backward(const void *dy, int dydt, const void *z, int zdt, int act, int64_t M,
+                                          int64_t N, void *dz, float *dbias, void *ws, size_t ws_bytes,
+                                          void *stream);
+
+/* The STE gradient products on the tensor cores, for many tokens: the same
+ * dx = gamma dz . W_q and dW = gamma dz^T . x_deq as bitlinear_backward_dx /
+ * _dw, from a bf16 gradient dz [M, N] and with fp32 sums instead of fp64:
+ *   dx: the products are exact (bf16 x {-1, 0, 1});
+ *   dW: dz s_m is rounded to fp32 and carried as two fp16 parts (22 bits,
+ *       scaled by a power of two per output row n, so that the row's largest
+ *       entry is near 2^13), times the exact x_q.
+ * Both add runs of contracted elements (512 for dx, 256 for dW) on the tensor
+ * core in fp32 and the runs in fp32 registers in order: the same bits on every
+ * call.  The error is below 2^-16 sum |terms| (at most 32 truncating additions
+ * a run).
+ *   packed, fmt, gamma  as for bitlinear_forward.
+ *   dx   [M, K] BL_F32 or BL_BF16;  dw [N, K] fp32 (zeros when M is 0).
+ *   xq, scale           the forward's codes and scales.
+ *   ws   at least the query's size (dx: a bf16 copy of the codes, N K 2 bytes;
+ *        dW: two fp16 planes of dz and one of x_q). */
+BL_API size_t bitlinear_backward_dx_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt);
+BL_API bl_status bitlinear_backward_dx_bf16(const uint8_t *packed, int fmt, const float *gamma, int64_t N, int64_t K,
+                                         const void *dz, int64_t M, void *dx, int dxdt, void *ws, size_t ws_bytes,
+                                         void *stream);
+BL_API size_t bitlinear_backward_dw_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K);
+BL_API bl_status bitlinear_backward_dw_bf16(const void *dz, const int8_t *xq, const float *scale, const float *gamma,
+                                         int64_t M, int64_t N, int64_t K, float *dw, void *ws, size_t ws_bytes,
+                                         void *stream);
+
+/* The norms around a block's end, with its gate and residual scale, for a
+ * block's output b and the residual stream r (one token per row, K values):
+ *   u = norm_post(b) * post_w + post_b       the norm after the block
+ *   h = res_scale r + branch_scale gate u    the new residual stream
+ *   y = norm_pre(h) * pre_w + pre_b          the norm before the next block
+ *   xq, scale = the INT8 codes of y (bitlinear_quantize_acts on the fp32 y)
+ * RMS: v / sqrt(mean v^2 + eps);  LAYER: (v - mean v) / sqrt(var v + eps) with
+ * the biased variance;  NONE: v.  Everything is computed in fp32 (sums in a
+ * fixed order) and rounded once where it is stored; norm_pre sees the
+ * unrounded h.  Feeds bitlinear_forward with xdt = BL_I8, or with y. */
+typedef enum { BL_NORM_NONE = 0, BL_NORM_RMS = 1, BL_NORM_LAYER = 2 } bl_norm;
+typedef struct {
+  int post;             /* bl_norm of the block's output */
+  float post_eps;       /* > 0 and finite unless post is BL_NORM_NONE */
+  const float *post_w;  /* [K], or NULL (1) */
+  const float *post_b;  /* [K], or NULL (0) */
+  const float *gate;    /* [ceil(M / gate_rows), K], or NULL (1) */
+  int64_t gate_rows;    /* token m uses gate row m / gate_rows (>= M: one shared row); >= 1 with a gate */
+  float res_scale;      /* finite */
+  float branch_scale;   /* finite */
+  int pre;              /* bl_norm of h */
+  float pre_eps;
+  const float *pre_w;   /* [K], or NULL (1) */
+  const float *pre_b;   /* [K], or NULL (0) */
+} bl_residual_norm_params;
+/*   b  [M, K] of type bdt;  r, h [M, K] of type rdt (h may be r, or NULL).
+ *   y  [M, K] of type ydt, or NULL;  xq [M, K] int8 with scale [M] fp32, or
+ *   both NULL.  At least one of h, y, xq is given. */
+BL_API bl_status bitlinear_residual_norm(const bl_residual_norm_params *p, const void *b, int bdt, const void *r,
+                                      int rdt, int64_t M, int64_t K, void *h, void *y, int ydt, int8_t *xq,
+                                      float *scale, void *stream);
+
+/* Its gradients, from dy (of y) and dh (of h through the residual stream):
+ *   dy   [M, K] of type dydt;  dh [M, K] of type rdt, or NULL (0);
+ *   b    [M, K] of type bdt and h [M, K] of type rdt as the forward had and
+ *        wrote them (statistics are recomputed from them);
+ *   dr   [M, K] of type rdt (may be dh), or NULL;  db [M, K] of type bdt (may
+ *        be dy when the types agree), or NULL;
+ *   dpost_w, dpost_b, dpre_w, dpre_b [K] fp32, dgate like gate, each or NULL
+ *        (the sums over tokens in fp32, in a fixed order: the same bits on
+ *        every call; zeros when M is 0).  dgate needs a gate.
+ *   ws   at least bitlinear_residual_norm_backward_workspace_bytes(M, K,
+ *        gate_rows) (gate_rows 0: no gate). */
+typedef struct {
+  float *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
+} bl_residual_norm_grads;
+BL_API size_t bitlinear_residual_norm_backward_workspace_bytes(int64_t M, int64_t K, int64_t gate_rows);
+BL_API bl_status bitlinear_residual_norm_backward(const bl_residual_norm_params *p, const void *dy, int dydt,
+                                               const void *dh, const void *b, int bdt, const void *h, int rdt,
+                                               int64_t M, int64_t K, void *dr, void *db,
+                                               const bl_residual_norm_grads *g, void *ws, size_t ws_bytes,
+                                               void *stream);
+
 /* Failure-detection self test: launches the tensor-core kernel with its data
  * producer switched off and a wait limit of about a millisecond, so that its
  * bounded waits run out; the kernel then records BL_ERR_DEVICE_TIMEOUT in the
