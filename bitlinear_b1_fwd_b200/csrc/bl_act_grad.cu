@@ -3,11 +3,13 @@
 //   dz[m, n] = dy[m, n] act'(z[m, n]),   dbias[n] = sum_m dz[m, n]
 //
 // One pass over dy and z: bound by HBM (3 values moved per element against
-// some 20 operations), so a thread takes 8 neighbouring columns (16-byte loads
-// of bf16) of several rows and keeps their column sums in registers.  A block
-// is 32 column threads x 8 row threads over a range of rows; its 8 row sums
-// meet in shared memory and go to a partial row, and column_sum_kernel adds
-// the partial rows in order (no atomics: the same bits on every call).
+// some 10 operations).  A thread takes 8 neighbouring columns (16-byte loads of
+// bf16) and keeps four of its rows in flight, their column sums in registers;
+// the activation is a template argument, so the inner loop has no choice in it.
+// A block is 32 column threads x 8 row threads over a range of rows; all blocks
+// are resident at once (one wave).  A block's 8 row sums meet in shared memory
+// and go to a partial row, and column_sum_kernel adds the partial rows in a
+// fixed order (no atomics: the same bits on every call).
 #include "bl_common.cuh"
 #include "bl_epilogue.cuh"
 #include "bl_kernels.h"
@@ -18,62 +20,70 @@ namespace {
 
 constexpr int kAgCols = 32, kAgRows = 8;  // threads of a block along columns and rows
 constexpr int kAgUnroll = 4;              // rows a thread has in flight
+constexpr int kAgResident = 4;            // blocks that fit an SM together (64 registers a thread)
 
 // act'(z).  For bf16 gradients the fast exponential and divide: their errors
 // (below 2^-20 for |z| < 30) are far under half a bf16 step, 2^-9.
-template <bool FAST>
-__device__ __forceinline__ float act_slope(int act, float z) {
-  switch (act) {
-    case BL_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case BL_ACT_RELU2: return z > 0.0f ? 2.0f * z : 0.0f;
-    case BL_ACT_SILU: {
-      const float s = FAST ? __fdividef(1.0f, 1.0f + __expf(-z)) : __fdiv_rn(1.0f, 1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case BL_ACT_GELU: {
-      const float t = -0.5f * z * z;
-      const float pdf = 0.39894228040143268f * (FAST ? __expf(t) : expf(t));
-      return 0.5f * erfcf(-0.70710678118654752f * z) + z * pdf;
-    }
-    default: return 1.0f;
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == BL_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (ACT == BL_ACT_RELU2) return z > 0.0f ? 2.0f * z : 0.0f;
+  if constexpr (ACT == BL_ACT_SILU) {
+    const float s = FAST ? __fdividef(1.0f, 1.0f + __expf(-z)) : __fdiv_rn(1.0f, 1.0f + expf(-z));
+    return s * (1.0f + z * (1.0f - s));
   }
+  if constexpr (ACT == BL_ACT_GELU) {
+    const float t = -0.5f * z * z;
+    const float pdf = 0.39894228040143268f * (FAST ? __expf(t) : expf(t));
+    return 0.5f * erfcf(-0.70710678118654752f * z) + z * pdf;
+  }
+  return 1.0f;
 }
 
-template <int DYT, int ZT, int VEC>
+template <int DYT, int ZT, int VEC, int ACT>
 __global__ void __launch_bounds__(kAgCols* kAgRows)
-    act_grad_kernel(const void* __restrict__ dy, const void* __restrict__ z, int act, int64_t M, int64_t N,
-                    int64_t rows_per, void* __restrict__ dz, float* __restrict__ part) {
+    act_grad_kernel(const void* __restrict__ dy, const void* __restrict__ z, int64_t M, int64_t N, int64_t rows_per,
+                    void* __restrict__ dz, float* __restrict__ part) {
   pdl_enter(dy, z, dz, part);
   __shared__ float sums[kAgRows][kAgCols * VEC + 1];
   const int tx = threadIdx.x % kAgCols, ty = threadIdx.x / kAgCols;
   const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * kAgCols + tx) * VEC;
   const int64_t m0 = blockIdx.y * rows_per, m1 = m0 + rows_per < M ? m0 + rows_per : M;
-  const bool live = n0 < N;
   float sum[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
-  if (live) {
-    for (int64_t m = m0 + ty; m < m1; m += kAgRows * kAgUnroll) {
-      float g[kAgUnroll][VEC], v[kAgUnroll][VEC];
+  auto one = [&](const Raw<DYT, VEC>& rg, const Raw<ZT, VEC>& rz, int64_t e) {
+    float g[VEC], v[VEC];
+    rg.get(g);
+    if constexpr (ACT != BL_ACT_NONE) rz.get(v);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if constexpr (ACT != BL_ACT_NONE) g[j] = __fmul_rn(g[j], act_slope<ACT, DYT == BL_BF16>(v[j]));
+      sum[j] += g[j];
+    }
+    if (dz != nullptr) store_vec<DYT, VEC>(dz, e, g);
+  };
+  if (n0 < N) {
+    int64_t m = m0 + ty;
+    const int64_t step = kAgRows * N;
+    for (; m + (kAgUnroll - 1) * kAgRows < m1; m += kAgRows * kAgUnroll) {
+      Raw<DYT, VEC> rg[kAgUnroll];
+      Raw<ZT, VEC> rz[kAgUnroll];
+      const int64_t e = m * N + n0;
 #pragma unroll
       for (int u = 0; u < kAgUnroll; ++u) {
-        const int64_t e = (m + u * kAgRows) * N + n0;
-        if (m + u * kAgRows < m1) {
-          load_vec<DYT, VEC>(dy, e, g[u]);
-          if (act != BL_ACT_NONE) load_vec<ZT, VEC>(z, e, v[u]);
-        }
+        rg[u].load(dy, e + u * step);
+        if constexpr (ACT != BL_ACT_NONE) rz[u].load(z, e + u * step);
       }
 #pragma unroll
-      for (int u = 0; u < kAgUnroll; ++u) {
-        if (m + u * kAgRows < m1) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            if (act != BL_ACT_NONE) g[u][j] *= act_slope<DYT == BL_BF16>(act, v[u][j]);
-            sum[j] += g[u][j];
-          }
-          if (dz != nullptr) store_vec<DYT, VEC>(dz, (m + u * kAgRows) * N + n0, g[u]);
-        }
-      }
+      for (int u = 0; u < kAgUnroll; ++u) one(rg[u], rz[u], e + u * step);
+    }
+    for (; m < m1; m += kAgRows) {
+      Raw<DYT, VEC> rg;
+      Raw<ZT, VEC> rz;
+      rg.load(dy, m * N + n0);
+      if constexpr (ACT != BL_ACT_NONE) rz.load(z, m * N + n0);
+      one(rg, rz, m * N + n0);
     }
   }
   if (part == nullptr) return;
@@ -91,16 +101,27 @@ __global__ void __launch_bounds__(kAgCols* kAgRows)
   }
 }
 
-// out[n] = sum over the partial rows, in order
-__global__ void __launch_bounds__(128)
+// out[n] = sum over the partial rows in a fixed order: 8 threads per column
+// each add every eighth row, their sums meet in order
+__global__ void __launch_bounds__(256)
     column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t N, float* __restrict__ out) {
   pdl_enter(part, out);
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float sums[8][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + tx;
   float s = 0.0f;
+  if (n < N) {
 #pragma unroll 8
-  for (int64_t r = 0; r < rows; ++r) s += __ldcg(part + r * N + n);
-  out[n] = s;
+    for (int64_t r = ty; r < rows; r += 8) s += __ldcg(part + r * N + n);
+  }
+  sums[ty][tx] = s;
+  __syncthreads();
+  if (ty == 0 && n < N) {
+    s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s += sums[r][tx];
+    out[n] = s;
+  }
 }
 
 int64_t col_blocks(int64_t N, int vec) { return (N + kAgCols * vec - 1) / (kAgCols * vec); }
@@ -109,17 +130,23 @@ template <int DYT, int ZT, int VEC>
 cudaError_t launch_t(const void* dy, const void* z, int act, int64_t M, int64_t N, void* dz, float* part,
                      int64_t blocks, cudaStream_t st) {
   const int64_t rows_per = (M + blocks - 1) / blocks;
-  return launch_pdl(act_grad_kernel<DYT, ZT, VEC>,
-                    dim3(static_cast<unsigned>(col_blocks(N, VEC)), static_cast<unsigned>(blocks)), kAgCols * kAgRows,
-                    0, st, dy, z, act, M, N, rows_per, dz, part);
+  const dim3 grid(static_cast<unsigned>(col_blocks(N, VEC)), static_cast<unsigned>(blocks));
+  auto run = [&](auto kern) { return launch_pdl(kern, grid, kAgCols * kAgRows, 0, st, dy, z, M, N, rows_per, dz, part); };
+  switch (act) {
+    case BL_ACT_RELU: return run(act_grad_kernel<DYT, ZT, VEC, BL_ACT_RELU>);
+    case BL_ACT_RELU2: return run(act_grad_kernel<DYT, ZT, VEC, BL_ACT_RELU2>);
+    case BL_ACT_SILU: return run(act_grad_kernel<DYT, ZT, VEC, BL_ACT_SILU>);
+    case BL_ACT_GELU: return run(act_grad_kernel<DYT, ZT, VEC, BL_ACT_GELU>);
+    default: return run(act_grad_kernel<DYT, DYT, VEC, BL_ACT_NONE>);
+  }
 }
 
 }  // namespace
 
-// Row blocks: enough for eight blocks per SM, each of at least kAgRows rows.
+// Row blocks: one wave of kAgResident blocks per SM, each of at least kAgRows rows.
 int64_t act_grad_row_blocks(int64_t M, int64_t N) {
   const int vec = N % 8 == 0 ? 8 : 1;
-  const int64_t want = (8 * static_cast<int64_t>(device_sms()) + col_blocks(N, vec) - 1) / col_blocks(N, vec);
+  const int64_t want = kAgResident * static_cast<int64_t>(device_sms()) / col_blocks(N, vec);
   const int64_t most = (M + kAgRows - 1) / kAgRows;
   int64_t b = want < most ? want : most;
   if (b > 65535) b = 65535;  // grid.y
@@ -149,7 +176,7 @@ cudaError_t launch_act_grad(const void* dy, int dydt, const void* z, int zdt, in
 #undef BL_AG
   if (e != cudaSuccess) return e;
   if (dbias != nullptr && blocks > 1)
-    e = launch_pdl(column_sum_kernel, static_cast<unsigned>((N + 127) / 128), 128, 0, st,
+    e = launch_pdl(column_sum_kernel, static_cast<unsigned>((N + 31) / 32), 256, 0, st,
                    static_cast<const float*>(part), blocks, N, dbias);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

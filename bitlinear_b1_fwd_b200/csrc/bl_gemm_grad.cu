@@ -42,6 +42,8 @@ constexpr int kTile = 128;   // rows of A, and columns of B, staged per CTA
 constexpr int kBR = 64;      // contracted elements per stage: 128 bytes, four MMAs of 16
 constexpr uint32_t kPlane = kTile * kBR * 2;  // 16384 bytes: one staged operand plane
 constexpr int kGradThreads = 320;             // warp 0 TMA, 1 MMA, 2-9 epilogue
+constexpr int kGradEpiWarps = 8;
+constexpr uint32_t kOutBox = 32 * 128;        // output staging of a warp: 32 rows of 128 bytes
 constexpr uint32_t kGradTmemCols = 512;       // two accumulators of 256 columns
 constexpr long long kGradTimeout = 1ll << 32;  // ~2 s at 1.9 GHz
 
@@ -51,7 +53,7 @@ struct GradCfg {
   static constexpr uint32_t kStage = (kPlanesA + 1) * kPlane;
   static constexpr int kStages = DW ? 4 : 6;
   static constexpr int kRun = DW ? 4 : 8;  // stages (32 MMAs) added up in tensor memory before the registers take over
-  static constexpr size_t kSmem = 1024 + kStages * kStage + 8 * (2 * kStages + 5) + 16;
+  static constexpr size_t kSmem = 1024 + kStages * kStage + kGradEpiWarps * kOutBox + 8 * (2 * kStages + 5) + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -113,8 +115,8 @@ __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
 template <bool DW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     gemm_grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a2,
-                     const __grid_constant__ CUtensorMap tm_b, const float* __restrict__ gamma,
-                     const float* __restrict__ rowinv, void* __restrict__ out, int odt, int I, int J, int R, int ks,
+                     const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_o, int o_tma,
+                     const float* __restrict__ gamma, const float* __restrict__ rowinv, void* __restrict__ out, int odt, int I, int J, int R, int ks,
                      float* __restrict__ part, WsHeader* __restrict__ hdr, long long limit) {
   pdl_enter(gamma, rowinv, out, part, hdr);
   using Cfg = GradCfg<DW>;
@@ -122,7 +124,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;  // S x [A planes, B plane], each 16 KB, swizzled
-  uint64_t* full = reinterpret_cast<uint64_t*>(stages + S * Cfg::kStage);  // leader: the loads of both CTAs
+  uint8_t* outs = stages + S * Cfg::kStage;  // an output box per epilogue warp, swizzled
+  uint64_t* full = reinterpret_cast<uint64_t*>(outs + kGradEpiWarps * kOutBox);  // leader: the loads of both CTAs
   uint64_t* empty = full + S;                                              // local: the MMAs have read the stage
   uint64_t* accf = empty + S;                                              // local: a run is in tensor memory (2)
   uint64_t* acce = accf + 2;                                               // leader: both CTAs have taken it (2)
@@ -298,33 +301,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + a), 0));
       }
       if (!ok) break;
-      const int i = w.it * 2 * kTile + static_cast<int>(rank) * kTile + 32 * q + lane;
+      const int i0 = w.it * 2 * kTile + static_cast<int>(rank) * kTile + 32 * q, i = i0 + lane;
       const int j0 = w.jt * 2 * kTile + half * kTile;
-      if (i < I) {
-        float alpha = 1.0f;
-        void* dst = out;
-        int dt = odt;
-        int64_t o = static_cast<int64_t>(i) * J + j0;
-        if (ks > 1) {
-          dst = part;
-          dt = BL_F32;
-          o += static_cast<int64_t>(w.kz) * I * J;
+      const bool f32 = ks > 1 || odt == BL_F32;
+      const float alpha = ks > 1 ? 1.0f
+                          : DW   ? (i < I ? __fmul_rn(__fdiv_rn(g, 127.0f), __ldcg(rowinv + i)) : 0.0f)
+                                 : g;
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) sum[j] = __fmul_rn(sum[j], alpha);
+      if (o_tma) {
+        // 32 rows x 128 bytes at a time through this warp's box; the TMA unit
+        // clips rows past I and columns past J
+        uint8_t* box = outs + (warp - 2) * kOutBox;
+        uint8_t* row = box + lane * 128;
+        auto put = [&](int c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = make_uint4(a0, a1, a2, a3);
+        };
+        auto store = [&](int j) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && i0 < I && j0 + j < J) tma_store_3d(&tm_o, box, j0 + j, i0, ks > 1 ? w.kz : 0);
+          if (lane == 0) bulk_commit();
+        };
+        auto box_free = [&]() {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+        };
+        if (f32) {
+#pragma unroll
+          for (int j = 0; j < kTile; j += 32) {
+            box_free();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              put(c, __float_as_uint(sum[j + 4 * c]), __float_as_uint(sum[j + 4 * c + 1]),
+                  __float_as_uint(sum[j + 4 * c + 2]), __float_as_uint(sum[j + 4 * c + 3]));
+            store(j);
+          }
         } else {
-          alpha = DW ? __fmul_rn(__fdiv_rn(g, 127.0f), __ldcg(rowinv + i)) : g;
+#pragma unroll
+          for (int j = 0; j < kTile; j += 64) {
+            box_free();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float* v = sum + j + 8 * c;
+              put(c, bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+            }
+            store(j);
+          }
         }
+      } else if (i < I) {
+        void* dst = ks > 1 ? part : out;
+        const int64_t o = (ks > 1 ? static_cast<int64_t>(w.kz) * I * J : 0) + static_cast<int64_t>(i) * J + j0;
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) sum[j] = __fmul_rn(sum[j], alpha);
-        if (J % 8 == 0) {
-#pragma unroll
-          for (int j = 0; j < kTile; j += 8)
-            if (j0 + j < J) store_vec_dt<8>(dst, dt, o + j, sum + j);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (j0 + j < J) store_vec_dt<1>(dst, dt, o + j, sum + j);
-        }
+        for (int j = 0; j < kTile; ++j)
+          if (j0 + j < J) store_vec_dt<1>(dst, f32 ? BL_F32 : BL_BF16, o + j, sum + j);
       }
     }
+    if (o_tma && lane == 0) bulk_wait<0>();  // every output has landed before the CTA leaves
   }
 
   __syncthreads();
@@ -337,118 +370,229 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 }
 
 // The parts of a cut contraction, added in order; then the factor and the
-// rounding to the output's type (dx).
+// rounding to the output's type (dx).  V outputs per thread (n a multiple of V).
+template <int V>
 __global__ void __launch_bounds__(256)
     grad_parts_kernel(const float* __restrict__ part, int ks, int64_t n, const float* __restrict__ gamma,
                       void* __restrict__ out, int odt) {
   pdl_enter(part, gamma, out);
   const float g = __ldcg(gamma);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += stride) {
-    float s = __ldcg(part + e);
-    for (int z = 1; z < ks; ++z) s += __ldcg(part + z * n + e);
-    s = __fmul_rn(s, g);
-    store_vec_dt<1>(out, odt, e, &s);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x * V;
+  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * V; e < n; e += stride) {
+    float s[V], t[V];
+    load_vec<BL_F32, V>(part, e, s);
+#pragma unroll 4
+    for (int z = 1; z < ks; ++z) {
+      load_vec<BL_F32, V>(part, z * n + e, t);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] += t[j];
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = __fmul_rn(s[j], g);
+    store_vec_dt<V>(out, odt, e, s);
   }
 }
 
-// 2-bit rows as bf16 {-1, 0, 1} rows of ld elements (ld = K rounded up to 64):
-// one 16-byte packed segment (64 weights, padding decodes to 0) per thread.
+// 2-bit rows as bf16 {-1, 0, 1} rows of ld elements (ld = K rounded up to 64,
+// the weights of a 16-byte packed segment; padding decodes to 0): one packed
+// word (16 weights, 32 output bytes) per thread.  Digit d becomes the bytes
+// (lo, hi) = (80 BF), (00 00), (80 3F), picked by a byte permute whose selector
+// is d, 4 + d for each of two digits.
 __global__ void __launch_bounds__(256)
-    i2_to_bf16_kernel(const uint8_t* __restrict__ i2, int64_t segs, uint16_t* __restrict__ w) {
+    i2_to_bf16_kernel(const uint32_t* __restrict__ i2, int64_t words, uint16_t* __restrict__ w) {
   pdl_enter(i2, w);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t s = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; s < segs; s += stride) {
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(i2) + s);
-    const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-    uint4* dst = reinterpret_cast<uint4*>(w) + 8 * s;
+  int64_t s = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  auto expand = [&](uint32_t v, int64_t at) {
+    uint4* dst = reinterpret_cast<uint4*>(w) + 2 * at;
+    const uint32_t even = v & 0x33333333u, odd = (v >> 2) & 0x33333333u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2; ++i) {
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t d = (wd[i >> 1] >> (16 * (i & 1) + 4 * j)) & 0xfu;  // two digits
-        const uint32_t a = d & 3u, c = d >> 2;
-        // digit 0 -> 0xBF80 (-1), 1 -> 0, 2 -> 0x3F80 (+1)
-        const uint32_t ha = a == 1u ? 0u : (a == 0u ? 0xbf80u : 0x3f80u);
-        const uint32_t hc = c == 1u ? 0u : (c == 0u ? 0xbf80u : 0x3f80u);
-        o[j] = ha | (hc << 16);
+        const uint32_t a = (even >> (16 * i + 4 * j)) & 0x3u, c = (odd >> (16 * i + 4 * j)) & 0x3u;
+        o[j] = __byte_perm(0x00800080u, 0x003f00bfu, a * 0x11u + c * 0x1100u + 0x4040u);
       }
       dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
+  };
+  for (; s + 3 * stride < words; s += 4 * stride) {
+    uint32_t v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = __ldcg(i2 + s + u * stride);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) expand(v[u], s + u * stride);
   }
+  for (; s < words; s += stride) expand(__ldcg(i2 + s), s);
 }
 
-// dz rows copied to a row stride of ld elements (a multiple of 8), for TMA.
+// dz rows copied to a row stride of ld elements (a multiple of 8, zeros past
+// N), for TMA: eight elements per thread.
 __global__ void __launch_bounds__(256)
     pad_rows_kernel(const uint16_t* __restrict__ src, int64_t M, int64_t N, int64_t ld, uint16_t* __restrict__ dst) {
   pdl_enter(src, dst);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x, n = M * ld;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += stride) {
-    const int64_t m = e / ld, c = e - m * ld;
-    dst[e] = c < N ? __ldcg(src + m * N + c) : static_cast<uint16_t>(0);
+  const int64_t per_row = ld / 8, items = M * per_row;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < items; e += stride) {
+    const int64_t m = e / per_row, c = 8 * (e - m * per_row);
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < N ? __ldcg(src + m * N + c + j) : 0u;
+    reinterpret_cast<uint4*>(dst)[e] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
   }
 }
 
-// The largest |dz s_m| of each output row n over a range of tokens, as bits
-// (finite magnitudes order like unsigned integers): part[range][n].
-__global__ void __launch_bounds__(256)
-    grad_rowmax_kernel(const uint16_t* __restrict__ dz, const float* __restrict__ scale, int64_t M, int64_t N,
-                       int64_t rows_per, uint32_t* __restrict__ part) {
-  pdl_enter(dz, scale, part);
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (n >= N) return;
-  const int64_t m0 = blockIdx.y * rows_per, m1 = m0 + rows_per < M ? m0 + rows_per : M;
-  float mx = 0.0f;
-#pragma unroll 8
-  for (int64_t m = m0; m < m1; ++m)
-    mx = fmaxf(mx, fabsf(__fmul_rn(bf16_bits_to_f32(__ldcg(dz + m * N + n)), __ldcg(scale + m))));
-  part[blockIdx.y * N + n] = __float_as_uint(mx);
+// ---- dW's operands ------------------------------------------------------------------
+// Two passes over dz (the second finds much of it in L2), bound by HBM.  Blocks
+// of 32 column threads (8 neighbouring columns each) x 8 row threads over a
+// range of rows; the first launch also carries the conversion of x_q, the other
+// operand, in blocks of its own.
+constexpr int kGcCols = 256, kGcRows = 8, kGcUnroll = 4;
+
+// dz[m, n0 .. n0 + 7] (zeros past N)
+__device__ __forceinline__ void load_dz8(const uint16_t* dz, int64_t m, int64_t n0, int64_t N, bool wide, float* v) {
+  if (wide) {
+    if (n0 < N) {
+      load_vec<BL_BF16, 8>(dz, m * N + n0, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = n0 + j < N ? bf16_bits_to_f32(__ldcg(dz + m * N + n0 + j)) : 0.0f;
+  }
 }
 
-// 2^e with the largest |v| 2^e of the row in [2^13, 2^14) (|e| <= 126; a row of
-// zeros keeps 1), and its inverse.
-__global__ void __launch_bounds__(256)
-    grad_rowscale_kernel(const uint32_t* __restrict__ part, int64_t ranges, int64_t N, float* __restrict__ rowscale,
-                         float* __restrict__ rowinv) {
-  pdl_enter(part, rowscale, rowinv);
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (n >= N) return;
-  uint32_t mx = 0;
-  for (int64_t r = 0; r < ranges; ++r) mx = max(mx, __ldcg(part + r * N + n));
-  const int ex = static_cast<int>(mx >> 23);  // biased exponent (0: below 2^-126)
-  int e = mx == 0 ? 0 : 13 - (ex - 127);
-  e = e > 126 ? 126 : (e < -126 ? -126 : e);
-  rowscale[n] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-  rowinv[n] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+// 4 int8 -> 4 fp16: 0x6400 | (q + 128) is the fp16 1152 + q
+__device__ __forceinline__ uint2 i8x4_to_f16(uint32_t q) {
+  q ^= 0x80808080u;
+  const uint32_t a = __byte_perm(q, 0x64646464u, 0x4140), b = __byte_perm(q, 0x64646464u, 0x4342);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+  const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&ha), *reinterpret_cast<const uint32_t*>(&hb));
 }
 
-// hi and lo fp16 parts of v = fl(dz s_m) 2^e, rows of ld elements (zeros past N).
+// Blocks below max_blocks: the largest |dz s_m| of each column n over a range of
+// rows, as bits (finite magnitudes order like unsigned integers), to
+// part[range][n].  The others: x_q as fp16 rows of ldk elements (zeros past K).
+__global__ void __launch_bounds__(256)
+    grad_max_kernel(const uint16_t* __restrict__ dz, const float* __restrict__ scale, int64_t M, int64_t N,
+                    int64_t rows_per, uint32_t* __restrict__ part, const int8_t* __restrict__ xq, int64_t K,
+                    int64_t ldk, __half* __restrict__ x, int col_blocks, int max_blocks) {
+  pdl_enter(dz, scale, part, xq, x);
+  if (static_cast<int>(blockIdx.x) >= max_blocks) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x - max_blocks) * blockDim.x;
+    int64_t e = static_cast<int64_t>(blockIdx.x - max_blocks) * blockDim.x + threadIdx.x;
+    uint4* dst = reinterpret_cast<uint4*>(x);
+    if (K % 16 == 0) {  // 16 elements per item
+      const int64_t per_row = K / 16, items = M * per_row;
+#pragma unroll 2
+      for (; e < items; e += stride) {
+        const uint4 q = __ldcg(reinterpret_cast<const uint4*>(xq) + e);
+        const uint2 a = i8x4_to_f16(q.x), b = i8x4_to_f16(q.y), c = i8x4_to_f16(q.z), d = i8x4_to_f16(q.w);
+        const int64_t m = e / per_row, o = (m * ldk + 16 * (e - m * per_row)) / 8;
+        dst[o] = make_uint4(a.x, a.y, b.x, b.y);
+        dst[o + 1] = make_uint4(c.x, c.y, d.x, d.y);
+      }
+    } else {  // 8 elements per item
+      const int64_t per_row = ldk / 8, items = M * per_row;
+      for (; e < items; e += stride) {
+        const int64_t m = e / per_row, k = 8 * (e - m * per_row);
+        uint32_t q[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (k + j < K)
+            q[j >> 2] |= static_cast<uint32_t>(__ldcg(reinterpret_cast<const uint8_t*>(xq) + m * K + k + j))
+                         << (8 * (j & 3));
+        const uint2 a = i8x4_to_f16(q[0]), b = i8x4_to_f16(q[1]);
+        dst[e] = make_uint4(a.x, a.y, b.x, b.y);
+      }
+    }
+    return;
+  }
+  __shared__ uint32_t mx[kGcRows][kGcCols];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t cb = blockIdx.x % col_blocks, range = blockIdx.x / col_blocks;
+  const int64_t n0 = cb * kGcCols + 8 * tx;
+  const int64_t m0 = range * rows_per, m1 = m0 + rows_per < M ? m0 + rows_per : M;
+  const bool wide = N % 8 == 0;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if (n0 < N) {
+#pragma unroll kGcUnroll
+    for (int64_t m = m0 + ty; m < m1; m += kGcRows) {
+      float d[8];
+      load_dz8(dz, m, n0, N, wide, d);
+      const float s = __ldcg(scale + m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fmaxf(v[j], fabsf(__fmul_rn(d[j], s)));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mx[ty][8 * tx + j] = __float_as_uint(v[j]);
+  __syncthreads();
+  const int64_t n = cb * kGcCols + threadIdx.x;
+  if (n < N) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int r = 0; r < kGcRows; ++r) a = max(a, mx[r][threadIdx.x]);
+    part[range * N + n] = a;
+  }
+}
+
+// The two fp16 parts of v = fl(dz s_m) 2^e, rows of ld elements (zeros past N).
+// 2^e brings the column's largest |v| into [2^13, 2^14) (|e| <= 126; a column of
+// zeros keeps 1); its inverse goes to rowinv for the product's epilogue.
 __global__ void __launch_bounds__(256)
     grad_split_kernel(const uint16_t* __restrict__ dz, const float* __restrict__ scale,
-                      const float* __restrict__ rowscale, int64_t M, int64_t N, int64_t ld, __half* __restrict__ hi,
-                      __half* __restrict__ lo) {
-  pdl_enter(dz, scale, rowscale, hi, lo);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x, total = M * ld;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += stride) {
-    const int64_t m = e / ld, n = e - m * ld;
-    float v = 0.0f;
-    if (n < N)
-      v = __fmul_rn(__fmul_rn(bf16_bits_to_f32(__ldcg(dz + m * N + n)), __ldcg(scale + m)), __ldcg(rowscale + n));
-    const __half h = __float2half_rn(v);
-    hi[e] = h;
-    lo[e] = __float2half_rn(__fsub_rn(v, __half2float(h)));
+                      const uint32_t* __restrict__ part, int ranges, int64_t M, int64_t N, int64_t rows_per,
+                      int64_t ld, float* __restrict__ rowinv, __half* __restrict__ hi, __half* __restrict__ lo) {
+  pdl_enter(dz, scale, part, rowinv, hi, lo);
+  __shared__ float factor[kGcCols];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  {
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * kGcCols + threadIdx.x;
+    uint32_t mx = 0;
+    if (n < N) {
+#pragma unroll 16
+      for (int r = 0; r < ranges; ++r) mx = max(mx, __ldcg(part + r * N + n));
+    }
+    const int ex = static_cast<int>(mx >> 23);  // biased exponent (0: below 2^-126)
+    int e = mx == 0 ? 0 : 13 - (ex - 127);
+    e = e > 126 ? 126 : (e < -126 ? -126 : e);
+    factor[threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (blockIdx.y == 0 && n < N) rowinv[n] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   }
-}
-
-// x_q as fp16 rows of ld elements (zeros past K).
-__global__ void __launch_bounds__(256)
-    i8_to_f16_kernel(const int8_t* __restrict__ xq, int64_t M, int64_t K, int64_t ld, __half* __restrict__ x) {
-  pdl_enter(xq, x);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x, total = M * ld;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += stride) {
-    const int64_t m = e / ld, k = e - m * ld;
-    x[e] = __int2half_rn(k < K ? static_cast<int>(__ldcg(reinterpret_cast<const signed char*>(xq) + m * K + k)) : 0);
+  __syncthreads();
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kGcCols + 8 * tx;
+  if (n0 >= ld) return;
+  const int64_t m0 = blockIdx.y * rows_per, m1 = m0 + rows_per < M ? m0 + rows_per : M;
+  const bool wide = N % 8 == 0;
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = factor[8 * tx + j];
+#pragma unroll kGcUnroll
+  for (int64_t m = m0 + ty; m < m1; m += kGcRows) {
+    float d[8];
+    load_dz8(dz, m, n0, N, wide, d);
+    const float s = __ldcg(scale + m);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = __fmul_rn(__fmul_rn(d[2 * j], s), f[2 * j]), b = __fmul_rn(__fmul_rn(d[2 * j + 1], s), f[2 * j + 1]);
+      const __half2 hh = __floats2half2_rn(a, b);
+      const float2 back = __half22float2(hh);
+      const __half2 ll = __floats2half2_rn(__fsub_rn(a, back.x), __fsub_rn(b, back.y));
+      h[j] = *reinterpret_cast<const uint32_t*>(&hh);
+      l[j] = *reinterpret_cast<const uint32_t*>(&ll);
+    }
+    const int64_t o = (m * ld + n0) / 8;
+    reinterpret_cast<uint4*>(hi)[o] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(lo)[o] = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -461,7 +605,7 @@ template <bool DW>
 cudaError_t launch_product(const void* a, const void* a2, int64_t lda, const void* b, int64_t ldb, const float* gamma,
                            const float* rowinv, void* out, int odt, int64_t I, int64_t J, int64_t R, int ks,
                            float* part, void* ws, cudaStream_t st) {
-  CUtensorMap ta, ta2, tb;
+  CUtensorMap ta, ta2, tb, to;
   // A: [I, R] K-major (dx) or [R, I] (dW); B: [R, J]
   const bool ok =
       DW ? encode_2d_b16(&ta, a, static_cast<uint64_t>(I), static_cast<uint64_t>(R), static_cast<uint64_t>(lda) * 2, 64,
@@ -474,13 +618,18 @@ cudaError_t launch_product(const void* a, const void* a2, int64_t lda, const voi
                             64, kBR))
     return cudaErrorInvalidValue;
   if (!DW) memset(&ta2, 0, sizeof ta2);
+  const int o_tma = encode_out_3d(&to, ks > 1 ? part : out, ks > 1 || odt == BL_F32, static_cast<uint64_t>(J),
+                                  static_cast<uint64_t>(I), static_cast<uint64_t>(ks))
+                        ? 1
+                        : 0;
+  if (!o_tma) memset(&to, 0, sizeof to);
   auto kern = gemm_grad_kernel<DW>;
   const size_t smem = GradCfg<DW>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int64_t units = ((I + 2 * kTile - 1) / (2 * kTile)) * ((J + 2 * kTile - 1) / (2 * kTile)) * ks;
   const int64_t most = device_sms() / 2, pairs = units < most ? units : most;
-  return launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGradThreads, smem, st, ta, ta2, tb, gamma, rowinv, out,
+  return launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGradThreads, smem, st, ta, ta2, tb, to, o_tma, gamma, rowinv, out,
                     odt, static_cast<int>(I), static_cast<int>(J), static_cast<int>(R), ks, part,
                     static_cast<WsHeader*>(ws), kGradTimeout);
 }
@@ -507,19 +656,24 @@ int grad_dx_parts(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-int64_t grad_rowmax_ranges(int64_t M) {
-  const int64_t r = (M + 127) / 128;
-  const int64_t per = (M + 63) / 64;  // at most 64 ranges
-  return r <= 64 ? (r < 1 ? 1 : r) : (M + per - 1) / per;
+// Row ranges of the passes over dz: one wave of four blocks per SM, each range of
+// at least 8 rows.
+int64_t grad_rowmax_ranges(int64_t M, int64_t N) {
+  const int64_t cols = (N + kGcCols - 1) / kGcCols, want = 4 * static_cast<int64_t>(device_sms()) / cols;
+  const int64_t most = (M + kGcRows - 1) / kGcRows;
+  int64_t r = want < 1 ? 1 : (want > 32 ? 32 : want);
+  if (r > most) r = most < 1 ? 1 : most;
+  const int64_t per = (M + r - 1) / r;
+  return per > 0 ? (M + per - 1) / per : 1;
 }
 
 cudaError_t launch_i2_to_bf16(const uint8_t* i2, int64_t N, int64_t rowbytes, uint16_t* w, cudaStream_t st) {
-  const int64_t segs = N * (rowbytes / 16);
-  return launch_pdl(i2_to_bf16_kernel, flat_grid(segs), 256, 0, st, i2, segs, w);
+  const int64_t words = N * (rowbytes / 4);
+  return launch_pdl(i2_to_bf16_kernel, flat_grid(words), 256, 0, st, reinterpret_cast<const uint32_t*>(i2), words, w);
 }
 
 cudaError_t launch_pad_rows(const uint16_t* src, int64_t M, int64_t N, int64_t ld, uint16_t* dst, cudaStream_t st) {
-  return launch_pdl(pad_rows_kernel, flat_grid(M * ld), 256, 0, st, src, M, N, ld, dst);
+  return launch_pdl(pad_rows_kernel, flat_grid(M * ld / 8), 256, 0, st, src, M, N, ld, dst);
 }
 
 cudaError_t launch_grad_dx(const uint16_t* dz, int64_t lddz, const uint16_t* w, int64_t ldw, const float* gamma,
@@ -529,26 +683,25 @@ cudaError_t launch_grad_dx(const uint16_t* dz, int64_t lddz, const uint16_t* w, 
   cudaError_t e = launch_product<false>(dz, nullptr, lddz, w, ldw, gamma, nullptr, dx, dxdt, M, K, N, ks, part, ws, st);
   if (e != cudaSuccess) return e;
   if (ks > 1)
-    e = launch_pdl(grad_parts_kernel, flat_grid(M * K), 256, 0, st, static_cast<const float*>(part), ks, M * K, gamma,
-                   dx, dxdt);
+    e = M * K % 8 == 0 ? launch_pdl(grad_parts_kernel<8>, flat_grid(M * K / 8), 256, 0, st,
+                                    static_cast<const float*>(part), ks, M * K, gamma, dx, dxdt)
+                       : launch_pdl(grad_parts_kernel<1>, flat_grid(M * K), 256, 0, st,
+                                    static_cast<const float*>(part), ks, M * K, gamma, dx, dxdt);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_grad_dw(const uint16_t* dz, const int8_t* xq, const float* scale, const float* gamma, int64_t M,
                            int64_t N, int64_t K, float* dw, const GradDwScratch& s, void* ws, cudaStream_t st) {
-  const int64_t ranges = grad_rowmax_ranges(M), rows_per = (M + ranges - 1) / ranges;
+  const int64_t ranges = grad_rowmax_ranges(M, N), rows_per = (M + ranges - 1) / ranges;
   const int64_t ldn = grad_ld(N), ldk = grad_ld(K);
-  const unsigned nb = static_cast<unsigned>((N + 255) / 256);
-  cudaError_t e = launch_pdl(grad_rowmax_kernel, dim3(nb, static_cast<unsigned>(ranges)), 256, 0, st, dz, scale, M, N,
-                             rows_per, s.maxes);
+  const int cols = static_cast<int>((N + kGcCols - 1) / kGcCols), max_blocks = static_cast<int>(cols * ranges);
+  const int64_t items = M * (K % 16 == 0 ? K / 16 : ldk / 8);
+  cudaError_t e = launch_pdl(grad_max_kernel, static_cast<unsigned>(max_blocks) + flat_grid(items), 256, 0, st, dz,
+                             scale, M, N, rows_per, s.maxes, xq, K, ldk, static_cast<__half*>(s.x), cols, max_blocks);
   if (e == cudaSuccess)
-    e = launch_pdl(grad_rowscale_kernel, nb, 256, 0, st, static_cast<const uint32_t*>(s.maxes), ranges, N, s.rowscale,
-                   s.rowinv);
-  if (e == cudaSuccess)
-    e = launch_pdl(grad_split_kernel, flat_grid(M * ldn), 256, 0, st, dz, scale, static_cast<const float*>(s.rowscale),
-                   M, N, ldn, static_cast<__half*>(s.hi), static_cast<__half*>(s.lo));
-  if (e == cudaSuccess)
-    e = launch_pdl(i8_to_f16_kernel, flat_grid(M * ldk), 256, 0, st, xq, M, K, ldk, static_cast<__half*>(s.x));
+    e = launch_pdl(grad_split_kernel, dim3(static_cast<unsigned>(cols), static_cast<unsigned>(ranges)), 256, 0, st, dz,
+                   scale, static_cast<const uint32_t*>(s.maxes), static_cast<int>(ranges), M, N, rows_per, ldn,
+                   s.rowinv, static_cast<__half*>(s.hi), static_cast<__half*>(s.lo));
   if (e == cudaSuccess)
     e = launch_product<true>(s.hi, s.lo, ldn, s.x, ldk, gamma, s.rowinv, dw, BL_F32, N, K, M, 1, nullptr, ws, st);
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -36,7 +36,6 @@
 namespace bl {
 namespace {
 
-constexpr int kGemmThreads = 384;  // warp 0 TMA, 1 MMA, 4-7 expansion, 8-11 epilogue
 constexpr int kBN = 128;  // weight rows per tile = MMA M
 constexpr int kBK = 128;  // K per stage = 4 MMAs of K = 32
 constexpr uint32_t kPackedStage = kBN * kBK / 4;  // 4096 bytes
@@ -431,7 +430,10 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
         const int t0 = w.t_t * BT + j0;
         if (ks == 1 && ydt != BL_I32)
           epilogue_chunk<Cfg::kChunk>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy,
-                                      n < N ? M - t0 : 0);
+                                      n < N ? M - t0 : 0, [&](int j, float z) {
+                                        if (n < N && t0 + j < M)
+                                          store_out(ep.pre, ydt, static_cast<int64_t>(t0 + j) * ldy + n, z);
+                                      });
         if (ks > 1) {
           if (n < N) {
 #pragma unroll
@@ -561,6 +563,7 @@ __global__ void __launch_bounds__(256)
 constexpr int kStagesA = 5;  // TMA ring: x half + packed tile per stage
 constexpr int kStagesB = 5;  // expanded-weight ring
 constexpr uint32_t kYStage = 32 * 128 * 4;  // output staging: 32 tokens x 128 rows, up to 4 bytes each
+constexpr int kGemm2Threads = 512;          // warp 0 TMA, 1 MMA, 4-7 expansion, 8-15 epilogue
 
 template <int BT>
 struct Gemm2Cfg {
@@ -591,9 +594,10 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
 }
 
 template <int BT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
     gemm_i2_2sm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                       const __grid_constant__ CUtensorMap tm_y, int y_tma, const float* __restrict__ gamma,
+                       const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_p, int y_tma,
+                       const float* __restrict__ gamma,
                        const float* __restrict__ scale, void* __restrict__ y, int ydt, int M, int N, int K, int ldy,
                        WsHeader* __restrict__ hdr, long long limit, const Epilogue ep_arg) {
   pdl_enter(gamma, scale, y, hdr);
@@ -638,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf + a, 1);
-      mbar_init(acce + a, 8);
+      mbar_init(acce + a, 16);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -750,16 +754,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp >= 8) {
     // ------------------------------ epilogue (both CTAs) ------------------------
-    // Each 32-token chunk of the tile's accumulator is converted into a shared
-    // staging buffer laid out as the output tile [32 tokens x 128 rows] and
-    // written by one TMA tensor store (the TMA unit clips rows past N and
-    // tokens past M); two buffers alternate, a buffer being rewritten only after
-    // the store issued from it two chunks before has read it.  Without a tensor
-    // map for y (a row of y not a multiple of 16 bytes) the lanes store directly.
-    const int q = warp & 3, et = threadIdx.x - 256;
+    // Two groups of four warps take the 32-token chunks of the tile's accumulator
+    // in turn.  A chunk is converted into the group's shared staging buffer, laid
+    // out as the output tile [32 tokens x 128 rows], and written by one TMA
+    // tensor store (the TMA unit clips rows past N and tokens past M); a buffer
+    // is rewritten only after the stores issued from it have read it.  A bf16
+    // tile takes half the buffer: two of them alternate, or the other half holds
+    // the kept pre-activations, stored the same way.  Without a tensor map for y
+    // (a row of y not a multiple of 16 bytes) the lanes store directly.
+    const int q = warp & 3, et = threadIdx.x - 256, grp = (warp - 8) >> 2;
+    const bool issuer = (et & 127) == 0;  // issues its group's stores
+    uint8_t* stage = ystage + grp * kYStage;
     const uint32_t esz = (ydt == BL_BF16) ? 2u : 4u;
     const float g = __ldcg(gamma);
     const Epilogue ep = epilogue_after_wait(ep_arg);
+    const bool keep_tma = y_tma && ydt == BL_BF16 && ep.act >= 0 && ep.pre != nullptr;
+    const bool two_bufs = ydt == BL_BF16 && !keep_tma;
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
     int tc = 0, chunk = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++tc) {
       const int a = tc & 1;
@@ -768,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int n = nbase + 32 * q + lane;
       const float bias = (ep.bias != nullptr && n < N) ? __ldcg(ep.bias + n) : 0.0f;
       float* cf = cfac + a * BT;
-      for (int j = et; j < BT; j += 128) {
+      for (int j = et; j < BT; j += 256) {
         const int t = t_t * BT + j;
         cf[j] = (t < M && ydt != BL_I32) ? dequant_factor(g, __ldcg(scale + t)) : 0.0f;
       }
@@ -777,7 +788,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       asm volatile(
           "{\n\t.reg .pred pi, po;\n\t"
           "setp.ne.u32 pi, %1, 0;\n\t"
-          "bar.red.and.pred po, 1, 128, pi;\n\t"
+          "bar.red.and.pred po, 1, 256, pi;\n\t"
           "selp.u32 %0, 1, 0, po;\n\t}"
           : "=r"(ok_all)
           : "r"(ok_w)
@@ -788,38 +799,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_after();
 #pragma unroll 1
-      for (int j0 = 0; j0 < BT; j0 += 32, ++chunk) {
+      for (int j0 = 32 * grp; j0 < BT; j0 += 64, ++chunk) {
         uint32_t acc[32];
         tmem_load<32>(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * BT + j0), acc);
         const int t0 = t_t * BT + j0;
-        if (ydt != BL_I32)
-          epilogue_chunk<32>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy, n < N ? M - t0 : 0);
-        if (y_tma) {
-          uint8_t* sb = ystage + (chunk & 1) * kYStage;
-          if (chunk >= 2) {  // the store issued from this buffer two chunks ago has read it
-            if (et == 0) bulk_wait_read<1>();
-            asm volatile("bar.sync 2, 128;" ::: "memory");
+        uint8_t* sb = stage + (two_bufs ? (chunk & 1) * (kYStage / 2) : 0);
+        if (y_tma) {  // the stores issued from this buffer have read it
+          if (issuer) {
+            if (two_bufs)
+              bulk_wait_read<1>();
+            else
+              bulk_wait_read<0>();
           }
-          uint8_t* col = sb + (32 * q + lane) * esz;  // this lane's row in the staged tile
+          group_sync();
+        }
+        uint8_t* col = sb + (32 * q + lane) * esz;  // this lane's row in the staged tile
+        if (ydt != BL_I32)
+          epilogue_chunk<32>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy, n < N ? M - t0 : 0,
+                             [&](int j, float z) {
+                               if (keep_tma)
+                                 *reinterpret_cast<__nv_bfloat16*>(col + kYStage / 2 + j * 128 * 2) = __float2bfloat16_rn(z);
+                               else if (n < N && t0 + j < M)
+                                 store_out(ep.pre, ydt, static_cast<int64_t>(t0 + j) * ldy + n, z);
+                             });
+        if (y_tma) {
+          if (ydt == BL_BF16) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int v = static_cast<int>(acc[j]);
-            if (ydt == BL_I32) {
-              *reinterpret_cast<int32_t*>(col + j * 128 * 4) = v;
-            } else {
-              const float yv = __uint_as_float(acc[j]);
-              if (ydt == BL_F32)
-                *reinterpret_cast<float*>(col + j * 128 * 4) = yv;
-              else
-                *reinterpret_cast<__nv_bfloat16*>(col + j * 128 * 2) = __float2bfloat16_rn(yv);
-            }
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<__nv_bfloat16*>(col + j * 128 * 2) = __float2bfloat16_rn(__uint_as_float(acc[j]));
+          } else {  // fp32 bits or INT32 sums
+#pragma unroll
+            for (int j = 0; j < 32; ++j) *reinterpret_cast<uint32_t*>(col + j * 128 * 4) = acc[j];
           }
           fence_proxy_async_smem();
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-          if (et == 0 && nbase < N && t0 < M) {
+          group_sync();
+          if (issuer && nbase < N && t0 < M) {
             tma_store_2d(&tm_y, sb, nbase, t0);
+            if (keep_tma) tma_store_2d(&tm_p, sb + kYStage / 2, nbase, t0);
           }
-          if (et == 0) bulk_commit();
+          if (issuer) bulk_commit();
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -844,7 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + a), 0));
     }
-    if (y_tma && et == 0) bulk_wait<0>();  // every output store has landed before the CTA leaves
+    if (y_tma && issuer) bulk_wait<0>();  // every output store has landed before the CTA leaves
   }
 
   __syncthreads();
@@ -861,28 +879,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // the same weight), for the tensor-core path.  Item (n, t): the 16 base-3
 // bytes 16t .. 16t + 15 of row n (weights 80t .. 80t + 79; bytes past rb5 read
 // as padding, 121 = five weight-0 digits) become 160 bits, i.e. five 32-bit
-// words at byte 20t of the 2-bit row (words past rb2 are dropped).  A byte's
-// five codes come from a 256-entry table of 10-bit entries with one copy per
-// lane, so the 32 lookups of a warp are one conflict-free access.
+// words at byte 20t of the 2-bit row (words past rb2 are dropped).  With
+// q_i = floor(b / 3^i) the digits of b are d_i = q_i - 3 q_{i+1}, so its ten bits
+// are sum d_i 4^i = b + q_1 + 4 q_2 + 16 q_3 + 64 q_4: four divisions by 3 (the
+// multiply by 171 / 512, exact below 256), two bytes at a time in the 16-bit
+// halves of a register.  No table: the 32 KB one per block that this replaces
+// took longer to fill than a 3200 x 8640 matrix takes to transcode.
+__device__ __forceinline__ uint32_t t5_pair(uint32_t x) {  // two bytes at bits 0 and 16 -> two 10-bit fields there
+  const uint32_t over = ((x + 0x000d000du) >> 8 & 0x00010001u) * 0xffu;  // bytes 243..255: five weight-0 digits (121)
+  x = (x & ~over) | (0x00790079u & over);
+  const uint32_t q1 = (x * 171u >> 9) & 0x007f007fu;
+  const uint32_t q2 = (q1 * 171u >> 9) & 0x007f007fu;
+  const uint32_t q3 = (q2 * 171u >> 9) & 0x007f007fu;
+  const uint32_t q4 = (q3 * 171u >> 9) & 0x007f007fu;
+  return x + q1 + 4u * q2 + 16u * q3 + 64u * q4;
+}
+
 __global__ void __launch_bounds__(256)
     t5_to_i2_kernel(const uint8_t* __restrict__ t5, int64_t N, int64_t K, int64_t rb5, uint8_t* __restrict__ i2,
                     int64_t rb2) {
   pdl_enter(t5, i2);
-  __shared__ uint32_t lut[256][32];
-  for (int e = threadIdx.x; e < 256 * 32; e += blockDim.x) {
-    const int b = e >> 5;
-    uint32_t v = static_cast<uint32_t>(b), d = 0x155u;  // bytes 243..255: five weight-0 digits
-    if (b < 243) {
-      d = 0;
-      for (int i = 0; i < 5; ++i) {
-        d |= (v % 3) << (2 * i);
-        v /= 3;
-      }
-    }
-    lut[b][e & 31] = d;
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
   // items fit in 32 bits (N K <= 2^32 and an item covers 80 weights): 32-bit
   // index arithmetic, no 64-bit division per item
   const uint32_t per_row = static_cast<uint32_t>((rb2 + 19) / 20);
@@ -894,14 +910,18 @@ __global__ void __launch_bounds__(256)
     const uint4 v = 16 * static_cast<int64_t>(t) < rb5 ? __ldcg(reinterpret_cast<const uint4*>(t5 + n * rb5 + 16 * t))
                                  : make_uint4(0x79797979u, 0x79797979u, 0x79797979u, 0x79797979u);
     const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-    uint32_t out[6] = {0u, 0u, 0u, 0u, 0u, 0u};
+    uint64_t f[4];  // 40 bits of each packed word
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t d = lut[(wd[i >> 2] >> (8 * (i & 3))) & 0xffu][lane];
-      const int pos = 10 * i, w = pos >> 5, sh = pos & 31;
-      out[w] |= d << sh;
-      if (sh > 22) out[w + 1] |= d >> (32 - sh);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = t5_pair(wd[i] & 0x00ff00ffu), c = t5_pair((wd[i] >> 8) & 0x00ff00ffu);  // bytes 0, 2 and 1, 3
+      const uint32_t lo = (a & 0x3ffu) | (c & 0x3ffu) << 10, hi = a >> 16 | (c >> 16) << 10;
+      f[i] = static_cast<uint64_t>(lo) | static_cast<uint64_t>(hi) << 20;
     }
+    const uint32_t out[5] = {static_cast<uint32_t>(f[0]),
+                             static_cast<uint32_t>(f[0] >> 32) | static_cast<uint32_t>(f[1]) << 8,
+                             static_cast<uint32_t>(f[1] >> 24) | static_cast<uint32_t>(f[2]) << 16,
+                             static_cast<uint32_t>(f[2] >> 16) | static_cast<uint32_t>(f[3]) << 24,
+                             static_cast<uint32_t>(f[3] >> 8)};
     uint32_t* dst = reinterpret_cast<uint32_t*>(i2 + n * rb2) + 5 * t;
 #pragma unroll
     for (int j = 0; j < 5; ++j)
@@ -991,9 +1011,9 @@ bool encode_y(CUtensorMap* m, void* y, int ydt, int64_t M, int64_t N, int64_t ld
 template <int BT>
 cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int ks, int32_t* part, void* ws,
-                           long long limit, int skip_producer, cudaStream_t st, const Epilogue& ep) {
+                           long long limit, int skip_producer, cudaStream_t st, const Epilogue& ep, int64_t ldx) {
   CUtensorMap tx, tw;
-  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K), 128, BT,
+  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(ldx), 128, BT,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!encode_2d_u8(&tw, w, static_cast<uint64_t>(rb), static_cast<uint64_t>(N), static_cast<uint64_t>(rb),
@@ -1027,9 +1047,9 @@ cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const
 template <int BT>
 cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                             void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, void* ws, long long limit,
-                            cudaStream_t st, const Epilogue& ep) {
+                            cudaStream_t st, const Epilogue& ep, int64_t ldx) {
   CUtensorMap tx, tw;
-  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K), 128,
+  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(ldx), 128,
                     BT / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!encode_2d_u8(&tw, w, static_cast<uint64_t>(rb), static_cast<uint64_t>(N), static_cast<uint64_t>(rb),
@@ -1038,6 +1058,8 @@ cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, cons
   CUtensorMap ty;
   const int y_tma = encode_y(&ty, y, ydt, M, N, ldy, 32) ? 1 : 0;
   if (!y_tma) memset(&ty, 0, sizeof(ty));
+  CUtensorMap tp = ty;  // the kept pre-activations: laid out like y
+  if (y_tma && ep.act >= 0 && ep.pre != nullptr && !encode_y(&tp, ep.pre, ydt, M, N, ldy, 32)) return cudaErrorInvalidValue;
   auto kern = gemm_i2_2sm_kernel<BT>;
   const size_t smem = Gemm2Cfg<BT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1045,7 +1067,7 @@ cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, cons
   const int64_t tiles = ((N + 2 * kBN - 1) / (2 * kBN)) * ((M + BT - 1) / BT);
   const int64_t pairs_max = device_sms() / 2;
   const int64_t pairs = tiles < pairs_max ? tiles : pairs_max;
-  { const cudaError_t le_ = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGemmThreads, smem, st, tx, tw, ty, y_tma, gamma, scale, y, ydt,
+  { const cudaError_t le_ = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGemm2Threads, smem, st, tx, tw, ty, tp, y_tma, gamma, scale, y, ydt,
                                                                      static_cast<int>(M), static_cast<int>(N),
                                                                      static_cast<int>(K), static_cast<int>(ldy),
                                                                      static_cast<WsHeader*>(ws),
@@ -1087,17 +1109,41 @@ int gemm_split_k(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int32_t* part, void* ws,
-                           long long limit_cycles, int skip_producer, cudaStream_t st, const Epilogue& ep) {
+                           long long limit_cycles, int skip_producer, cudaStream_t st, const Epilogue& ep, int64_t ldx) {
   const long long limit = limit_cycles > 0 ? limit_cycles : kTimeoutCycles;
+  if (ldx == 0) ldx = K;
   if (M > 128 && !skip_producer)
-    return launch_gemm_2sm<256>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ws, limit, st, ep);
+    return launch_gemm_2sm<256>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ws, limit, st, ep, ldx);
   const int ks = (part != nullptr && !skip_producer) ? gemm_split_k(M, N, K) : 1;
   switch (gemm_token_tile(M)) {
-    case 16: return launch_gemm_bt<16>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
-    case 32: return launch_gemm_bt<32>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
-    case 64: return launch_gemm_bt<64>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
-    default: return launch_gemm_bt<128>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep);
+    case 16: return launch_gemm_bt<16>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
+    case 32: return launch_gemm_bt<32>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
+    case 64: return launch_gemm_bt<64>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
+    default: return launch_gemm_bt<128>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
   }
+}
+
+// x_q rows copied to a row stride of ld bytes (a multiple of 16, zeros past K),
+// for TMA: 16 codes per thread.
+__global__ void __launch_bounds__(256)
+    pad_codes_kernel(const uint8_t* __restrict__ src, int64_t M, int64_t K, int64_t ld, uint8_t* __restrict__ dst) {
+  pdl_enter(src, dst);
+  const int64_t per_row = ld / 16, items = M * per_row;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < items; e += stride) {
+    const int64_t m = e / per_row, k = 16 * (e - m * per_row);
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (k + j < K) v[j >> 2] |= static_cast<uint32_t>(__ldcg(src + m * K + k + j)) << (8 * (j & 3));
+    reinterpret_cast<uint4*>(dst)[e] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+cudaError_t launch_pad_codes(const int8_t* src, int64_t M, int64_t K, int64_t ld, int8_t* dst, cudaStream_t st) {
+  const int64_t cap = static_cast<int64_t>(device_sms()) * 8, g = (M * (ld / 16) + 255) / 256;
+  return launch_pdl(pad_codes_kernel, static_cast<unsigned>(g < cap ? g : cap), 256, 0, st,
+                    reinterpret_cast<const uint8_t*>(src), M, K, ld, reinterpret_cast<uint8_t*>(dst));
 }
 
 cudaError_t launch_b1_to_i2(const uint8_t* b1, int64_t N, int64_t K, int64_t rb1, uint8_t* i2, int64_t rb2,

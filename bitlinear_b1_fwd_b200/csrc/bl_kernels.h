@@ -77,7 +77,9 @@ int gemm_token_tile(int64_t M);
 cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int32_t* part, void* ws,
                            long long limit_cycles, int skip_producer, cudaStream_t st,
-                           const Epilogue& ep = no_epilogue());  // with an epilogue ldy == N
+                           const Epilogue& ep = no_epilogue(),  // with an epilogue ldy == N
+                           int64_t ldx = 0);  // row stride of xq (a multiple of 16); 0: K
+cudaError_t launch_pad_codes(const int8_t* src, int64_t M, int64_t K, int64_t ld, int8_t* dst, cudaStream_t st);
 int gemm_split_k(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_t5_to_i2(const uint8_t* t5, int64_t N, int64_t K, int64_t rb5, uint8_t* i2, int64_t rb2,
                             cudaStream_t st);
@@ -124,17 +126,17 @@ cudaError_t launch_act_grad(const void* dy, int dydt, const void* z, int zdt, in
 // where ks = grad_dx_parts(M, N, K) > 1.
 int64_t grad_ld(int64_t n);
 int grad_dx_parts(int64_t M, int64_t N, int64_t K);
-int64_t grad_rowmax_ranges(int64_t M);
+int64_t grad_rowmax_ranges(int64_t M, int64_t N);
 cudaError_t launch_i2_to_bf16(const uint8_t* i2, int64_t N, int64_t rowbytes, uint16_t* w, cudaStream_t st);
 cudaError_t launch_pad_rows(const uint16_t* src, int64_t M, int64_t N, int64_t ld, uint16_t* dst, cudaStream_t st);
 cudaError_t launch_grad_dx(const uint16_t* dz, int64_t lddz, const uint16_t* w, int64_t ldw, const float* gamma,
                            int64_t M, int64_t N, int64_t K, void* dx, int dxdt, float* part, void* ws,
                            cudaStream_t st);
 struct GradDwScratch {
-  uint32_t* maxes;           // [grad_rowmax_ranges(M)][N]
-  float *rowscale, *rowinv;  // [N]
-  void *hi, *lo;             // fp16 [M][grad_ld(N)]
-  void* x;                   // fp16 [M][grad_ld(K)]
+  uint32_t* maxes;  // [grad_rowmax_ranges(M, N)][N]
+  float* rowinv;    // [N]
+  void *hi, *lo;    // fp16 [M][grad_ld(N)]
+  void* x;          // fp16 [M][grad_ld(K)]
 };
 cudaError_t launch_grad_dw(const uint16_t* dz, const int8_t* xq, const float* scale, const float* gamma, int64_t M,
                            int64_t N, int64_t K, float* dw, const GradDwScratch& s, void* ws, cudaStream_t st);

@@ -38,4 +38,20 @@ inline bool encode_2d_b16(CUtensorMap* m, const void* base, uint64_t inner, uint
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [planes x rows x cols] of a 4- or 2-byte float type written by TMA stores from
+// swizzled boxes of 128 bytes x 32 rows.  False when a row is not a multiple of
+// 16 bytes.
+inline bool encode_out_3d(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t planes) {
+  const uint64_t esz = f32 ? 4 : 2;
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr || cols * esz % 16 != 0) return false;
+  const cuuint64_t dims[3] = {cols, rows, planes};
+  const cuuint64_t strides[2] = {cols * esz, rows * cols * esz};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esz), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace bl

@@ -18,6 +18,47 @@ __device__ __forceinline__ void load_vec(const void* p, int64_t e, float* v) {
     v[0] = load_elem<DT>(p, e);
   }
 }
+// VEC consecutive elements as loaded, widened when they are used.
+template <int DT, int VEC>
+struct Raw;
+template <>
+struct Raw<BL_BF16, 8> {
+  uint4 q;
+  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    q = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e));
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw<BL_F32, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
+    a = __ldcg(q);
+    b = __ldcg(q + 1);
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <int DT>
+struct Raw<DT, 1> {
+  float f;
+  __device__ __forceinline__ void zero() { f = 0.0f; }
+  __device__ __forceinline__ void load(const void* p, int64_t e) { f = load_elem<DT>(p, e); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = f; }
+};
+
 template <int VEC>
 __device__ __forceinline__ void load_vec_dt(const void* p, int dt, int64_t e, float* v) {
   if (dt == BL_F32)
@@ -58,37 +99,56 @@ __device__ __forceinline__ void store_vec_dt(void* p, int dt, int64_t e, const f
     store_vec<BL_BF16, VEC>(p, e, v);
 }
 
-// Sums of two values over the block in a fixed order, the same in every
+// Sums of one to four values over the block in a fixed order, the same in every
 // thread; one barrier.  Two buffers alternate: a buffer is written again only
 // after the barrier of the next sum, which every thread reaches after its
 // reads.
 struct BlockSum {
-  float2 (*buf)[32];  // shared [2][32]
+  float4 (*buf)[32];  // shared [2][32]
   int nw, phase;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
+  template <int N>
+  __device__ __forceinline__ void run(float (&a)[N]) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    float2* w = buf[phase];
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < N; ++j) a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
+    if (nw == 1) return;
+    float4* w = buf[phase];
     phase ^= 1;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) w[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 p = lane < nw ? w[lane] : make_float2(0.0f, 0.0f);
-    a = p.x;
-    b = p.y;
+    if (lane == 0) {
+      float* d = reinterpret_cast<float*>(w + (threadIdx.x >> 5));
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
+      for (int j = 0; j < N; ++j) d[j] = a[j];
     }
-    return make_float2(a, b);
+    __syncthreads();
+    const float* d = reinterpret_cast<const float*>(w + lane);
+#pragma unroll
+    for (int j = 0; j < N; ++j) a[j] = lane < nw ? d[j] : 0.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < N; ++j) a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
+  }
+  __device__ __forceinline__ float one(float a) {
+    float v[1] = {a};
+    run(v);
+    return v[0];
+  }
+  __device__ __forceinline__ float2 two(float a, float b) {
+    float v[2] = {a, b};
+    run(v);
+    return make_float2(v[0], v[1]);
+  }
+  __device__ __forceinline__ float4 four(float a, float b, float c, float d) {
+    float v[4] = {a, b, c, d};
+    run(v);
+    return make_float4(v[0], v[1], v[2], v[3]);
   }
   __device__ __forceinline__ float max(float a) {
     a = warp_maxf(a);
-    float2* w = buf[phase];
+    if (nw == 1) return a;
+    float4* w = buf[phase];
     phase ^= 1;
     const int lane = threadIdx.x & 31;
     if (lane == 0) w[threadIdx.x >> 5].x = a;
