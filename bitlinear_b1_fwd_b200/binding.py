@@ -283,21 +283,21 @@ def bitlinear_backward_dw(dy, xq, scale, gamma, dw, stream=None) -> None:
 # given); the current device of the caller does not change.
 
 _F32, _BF16, _INT8, _U8 = torch.float32, torch.bfloat16, torch.int8, torch.uint8
-_FLOATS = (_F32, _BF16)
+_FLOATS, _ONLY_F32, _ONLY_BF16, _ONLY_I8, _BYTES = (_F32, _BF16), (_F32,), (_BF16,), (_INT8,), (_U8,)
+_INPUTS = (_F32, _BF16, _INT8)
 
 
 def _want(name, t, shape, dtypes, dev):
     """t is None or a contiguous tensor of this shape and one of the dtypes on dev."""
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous()):
         return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _matrix(name, t):
@@ -312,25 +312,41 @@ def _matrix(name, t):
 def _workspace(ws, dev):
     if ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on {dev}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _raw(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle and the current device without building objects
+# (torch.cuda.current_stream() alone costs 3.2 us, as much as a launch)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _call(name, dev, stream, *args):
     """lib().name(*args, stream) on dev."""
     fn = getattr(_lib or lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = torch.cuda.current_stream() if stream is None else stream
-        status = fn(*args, st.cuda_stream)
+    index = dev.index
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = torch.cuda.current_stream() if stream is None else stream
-            status = fn(*args, st.cuda_stream)
+            status = fn(*args, handle)
     if status != BL_OK:
         raise BitLinearError(status, name)
+
+
+_PER_BYTE = {BL_PACK_I2: 4, BL_PACK_T5: 5, BL_PACK_B1: 8}
+
+
+def _packed_row(K, fmt):
+    """bitlinear_packed_row_bytes(K, fmt)"""
+    per = _PER_BYTE.get(fmt)
+    if per is None or K < 1:
+        return bitlinear_packed_row_bytes(K, fmt)
+    return (-(-K // per) + 15) // 16 * 16
 
 
 def bitlinear_forward_epilogue_workspace_bytes(M: int, N: int, K: int, fmt: int, xdt: int) -> int:
@@ -342,12 +358,12 @@ def bitlinear_forward_epilogue(packed, fmt, gamma, N, K, x, scale, y, ws, bias=N
     """y = act(x W_q^T dequantized + bias) + residual; preact receives the argument of act."""
     dev = _matrix("x", x)
     M = x.shape[0]
-    _want("x", x, (M, K), (_F32, _BF16, _INT8), dev)
-    _want("packed", packed, (N, bitlinear_packed_row_bytes(K, fmt)), (_U8,), dev)
-    _want("gamma", gamma, (1,), (_F32,), dev)
-    _want("scale", scale, (M,), (_F32,), dev)
+    _want("x", x, (M, K), _INPUTS, dev)
+    _want("packed", packed, (N, _packed_row(K, fmt)), _BYTES, dev)
+    _want("gamma", gamma, (1,), _ONLY_F32, dev)
+    _want("scale", scale, (M,), _ONLY_F32, dev)
     _want("y", y, (M, N), _FLOATS, dev)
-    _want("bias", bias, (N,), (_F32,), dev)
+    _want("bias", bias, (N,), _ONLY_F32, dev)
     _want("residual", residual, (M, N), (y.dtype,), dev)
     _want("preact", preact, (M, N), (y.dtype,), dev)
     wp, wn = _workspace(ws, dev)
@@ -367,7 +383,7 @@ def bitlinear_epilogue_backward(dy, z, act, dz, dbias, ws, stream=None) -> None:
     _want("dy", dy, (M, N), _FLOATS, dev)
     _want("z", z, (M, N), _FLOATS, dev)
     _want("dz", dz, (M, N), (dy.dtype,), dev)
-    _want("dbias", dbias, (N,), (_F32,), dev)
+    _want("dbias", dbias, (N,), _ONLY_F32, dev)
     wp, wn = _workspace(ws, dev)
     _call("bitlinear_epilogue_backward", dev, stream, dy.data_ptr(), _DT[dy.dtype], _raw(z),
           BL_F32 if z is None else _DT[z.dtype], act, M, N, _raw(dz), _raw(dbias), wp, wn)
@@ -381,9 +397,9 @@ def bitlinear_backward_dx_bf16(packed, fmt, gamma, N, K, dz, dx, ws, stream=None
     """dx = gamma dz W_q on the tensor cores (bf16 dz, dx bf16 or fp32)."""
     dev = _matrix("dz", dz)
     M = dz.shape[0]
-    _want("dz", dz, (M, N), (_BF16,), dev)
-    _want("packed", packed, (N, bitlinear_packed_row_bytes(K, fmt)), (_U8,), dev)
-    _want("gamma", gamma, (1,), (_F32,), dev)
+    _want("dz", dz, (M, N), _ONLY_BF16, dev)
+    _want("packed", packed, (N, _packed_row(K, fmt)), _BYTES, dev)
+    _want("gamma", gamma, (1,), _ONLY_F32, dev)
     _want("dx", dx, (M, K), _FLOATS, dev)
     wp, wn = _workspace(ws, dev)
     _call("bitlinear_backward_dx_bf16", dev, stream, packed.data_ptr(), fmt, gamma.data_ptr(), N, K, dz.data_ptr(), M,
@@ -399,11 +415,11 @@ def bitlinear_backward_dw_bf16(dz, xq, scale, gamma, dw, ws, stream=None) -> Non
     dev = _matrix("dz", dz)
     M, N = dz.shape
     K = xq.shape[-1]
-    _want("dz", dz, (M, N), (_BF16,), dev)
-    _want("xq", xq, (M, K), (_INT8,), dev)
-    _want("scale", scale, (M,), (_F32,), dev)
-    _want("gamma", gamma, (1,), (_F32,), dev)
-    _want("dw", dw, (N, K), (_F32,), dev)
+    _want("dz", dz, (M, N), _ONLY_BF16, dev)
+    _want("xq", xq, (M, K), _ONLY_I8, dev)
+    _want("scale", scale, (M,), _ONLY_F32, dev)
+    _want("gamma", gamma, (1,), _ONLY_F32, dev)
+    _want("dw", dw, (N, K), _ONLY_F32, dev)
     wp, wn = _workspace(ws, dev)
     _call("bitlinear_backward_dw_bf16", dev, stream, dz.data_ptr(), xq.data_ptr(), scale.data_ptr(), gamma.data_ptr(),
           M, N, K, dw.data_ptr(), wp, wn)
@@ -413,16 +429,19 @@ def _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res
                  pre_b, pre_eps):
     if gate is not None and gate_rows < 1:
         gate_rows = max(M, 1)       # one row for every token
-    for name, t in (("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w), ("pre_b", pre_b)):
-        _want(name, t, (K,), (_F32,), dev)
+    row = (K,)
+    _want("post_w", post_w, row, _ONLY_F32, dev)
+    _want("post_b", post_b, row, _ONLY_F32, dev)
+    _want("pre_w", pre_w, row, _ONLY_F32, dev)
+    _want("pre_b", pre_b, row, _ONLY_F32, dev)
     if gate is not None:
         rows = -(-M // gate_rows)
         if gate.dim() == 1:
-            _want("gate", gate, (K,), (_F32,), dev)
+            _want("gate", gate, (K,), _ONLY_F32, dev)
             if rows > 1:
                 raise ValueError(f"gate: one row, expected {rows}")
         else:
-            _want("gate", gate, (rows, K), (_F32,), dev)
+            _want("gate", gate, (rows, K), _ONLY_F32, dev)
     return ResidualNormParams(post, post_eps, _raw(post_w), _raw(post_b), _raw(gate), gate_rows if gate is not None else 0,
                               res_scale, branch_scale, pre, pre_eps, _raw(pre_w), _raw(pre_b))
 
@@ -439,8 +458,8 @@ def bitlinear_residual_norm(b, r, h, post=BL_NORM_NONE, post_w=None, post_b=None
     _want("r", r, (M, K), _FLOATS, dev)
     _want("h", h, (M, K), (r.dtype,), dev)
     _want("y", y, (M, K), _FLOATS, dev)
-    _want("xq", xq, (M, K), (_INT8,), dev)
-    _want("scale", scale, (M,), (_F32,), dev)
+    _want("xq", xq, (M, K), _ONLY_I8, dev)
+    _want("scale", scale, (M,), _ONLY_F32, dev)
     p = _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
                      pre_b, pre_eps)
     _call("bitlinear_residual_norm", dev, stream, C.addressof(p), b.data_ptr(), _DT[b.dtype], r.data_ptr(),
@@ -466,11 +485,11 @@ def bitlinear_residual_norm_backward(dy, dh, b, h, dr, db, ws, post=BL_NORM_NONE
     _want("dr", dr, (M, K), (h.dtype,), dev)
     _want("db", db, (M, K), (b.dtype,), dev)
     for name, t in (("dpost_w", dpost_w), ("dpost_b", dpost_b), ("dpre_w", dpre_w), ("dpre_b", dpre_b)):
-        _want(name, t, (K,), (_F32,), dev)
+        _want(name, t, (K,), _ONLY_F32, dev)
     if dgate is not None:
         if gate is None:
             raise ValueError("dgate without a gate")
-        _want("dgate", dgate, tuple(gate.shape), (_F32,), dev)
+        _want("dgate", dgate, tuple(gate.shape), _ONLY_F32, dev)
     p = _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
                      None, pre_eps)
     g = ResidualNormGrads(_raw(dpost_w), _raw(dpost_b), _raw(dgate), _raw(dpre_w), _raw(dpre_b))

@@ -4,7 +4,7 @@
 //
 // One pass over dy and z: bound by HBM (3 values moved per element against
 // some 10 operations).  A thread takes 8 neighbouring columns (16-byte loads of
-// bf16) and keeps four of its rows in flight, their column sums in registers;
+// bf16) and keeps some of its rows in flight, their column sums in registers;
 // the activation is a template argument, so the inner loop has no choice in it.
 // A block is 32 column threads x 8 row threads over a range of rows; all blocks
 // are resident at once (one wave).  A block's 8 row sums meet in shared memory
@@ -19,8 +19,9 @@ namespace bl {
 namespace {
 
 constexpr int kAgCols = 32, kAgRows = 8;  // threads of a block along columns and rows
-constexpr int kAgUnroll = 4;              // rows a thread has in flight
 constexpr int kAgResident = 4;            // blocks that fit an SM together (64 registers a thread)
+// rows a thread has in flight: what its 64 registers hold
+constexpr int ag_unroll(int dyt, int zt, int vec) { return vec == 8 && (dyt == BL_F32 || zt == BL_F32) ? 2 : 4; }
 
 // act'(z).  For bf16 gradients the fast exponential and divide: their errors
 // (below 2^-20 for |z| < 30) are far under half a bf16 step, 2^-9.
@@ -41,10 +42,11 @@ __device__ __forceinline__ float act_slope(float z) {
 }
 
 template <int DYT, int ZT, int VEC, int ACT>
-__global__ void __launch_bounds__(kAgCols* kAgRows)
+__global__ void __launch_bounds__(kAgCols* kAgRows, kAgResident)
     act_grad_kernel(const void* __restrict__ dy, const void* __restrict__ z, int64_t M, int64_t N, int64_t rows_per,
                     void* __restrict__ dz, float* __restrict__ part) {
   pdl_enter(dy, z, dz, part);
+  constexpr int kAgUnroll = ag_unroll(DYT, ZT, VEC);
   __shared__ float sums[kAgRows][kAgCols * VEC + 1];
   const int tx = threadIdx.x % kAgCols, ty = threadIdx.x / kAgCols;
   const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * kAgCols + tx) * VEC;

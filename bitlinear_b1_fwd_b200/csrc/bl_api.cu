@@ -82,13 +82,14 @@ bool b1_via_i2(int fmt, int64_t K) { return fmt == BL_PACK_B1 && (K + 7) / 8 > 4
 inline bool pads_codes(int64_t M, int64_t K) { return M > bl::kGemvMaxTokens && K % 16 != 0; }
 inline int64_t padded_codes(int64_t K) { return (K + 15) / 16 * 16; }
 
-static size_t forward_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt, bool pad) {
+static size_t forward_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt, bool pad, bool i8) {
   if (!m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
   size_t bytes = BL_WS_HEADER_BYTES;
   if (pad || uses_gemm(M, K)) {
     if (xdt != BL_I8) bytes += round256(static_cast<size_t>(M * K));
     if (pad) bytes += round256(static_cast<size_t>(M * padded_codes(K)));
     if (fmt != BL_PACK_I2) bytes += round256(static_cast<size_t>(N * bitlinear_packed_row_bytes(K, BL_PACK_I2)));
+    if (i8) bytes += round256(static_cast<size_t>(N * 4 * bitlinear_packed_row_bytes(K, BL_PACK_I2)));
     const int ks = bl::gemm_split_k(M, N, K);
     if (ks > 1) bytes += round256(static_cast<size_t>(ks) * M * N * sizeof(int32_t));
   } else if (b1_via_i2(fmt, K)) {
@@ -98,7 +99,7 @@ static size_t forward_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt, b
 }
 
 size_t bitlinear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
-  return forward_bytes(M, N, K, fmt, xdt, false);
+  return forward_bytes(M, N, K, fmt, xdt, false, false);
 }
 
 bl_status bitlinear_workspace_init(void* ws, size_t ws_bytes, void* stream) {
@@ -213,7 +214,8 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
       !aligned(gamma, 4) || !aligned(ws, 16))
     return BL_ERR_MISALIGNED;
   const bool pad = ep.act >= 0 && pads_codes(M, K);
-  if (ws_bytes < forward_bytes(M, N, K, fmt, xdt, pad)) return BL_ERR_WORKSPACE_TOO_SMALL;
+  const bool many = ep.act >= 0 && M >= bl::kGemmI8Tokens;
+  if (ws_bytes < forward_bytes(M, N, K, fmt, xdt, pad, many)) return BL_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pad && !uses_gemm(M, K)) {
     if (b1_via_i2(fmt, K)) {
@@ -251,6 +253,11 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
     w2 = scratch;
     scratch += round256(static_cast<size_t>(N * rb2));
   }
+  if (many && bl::gemm_i8_fits(M, N, ydt)) {
+    int8_t* w8 = reinterpret_cast<int8_t*>(scratch);
+    if (bl::launch_i2_to_i8(w2, N, rb2, w8, st) != cudaSuccess) return BL_ERR_CUDA;
+    return cuda_status(bl::launch_gemm_i8(xq, padded_codes(K), w8, 4 * rb2, gamma, scale, y, ydt, M, N, K, ep, ws, st));
+  }
   int32_t* part = bl::gemm_split_k(M, N, K) > 1 ? reinterpret_cast<int32_t*>(scratch) : nullptr;
   return cuda_status(bl::launch_gemm_i2(xq, w2, rb2, gamma, scale, y, ydt, M, N, K, N, part, ws, 0, 0, st, ep, padded_codes(K)));
 }
@@ -262,7 +269,7 @@ bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, 
 }
 
 size_t bitlinear_forward_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
-  return forward_bytes(M, N, K, fmt, xdt, pads_codes(M, K));
+  return forward_bytes(M, N, K, fmt, xdt, pads_codes(M, K), M >= bl::kGemmI8Tokens);
 }
 
 bl_status bitlinear_forward_epilogue(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
@@ -570,7 +577,7 @@ bl_status bitlinear_residual_norm(const bl_residual_norm_params* p, const void* 
 size_t bitlinear_residual_norm_backward_workspace_bytes(int64_t M, int64_t K, int64_t gate_rows) {
   if (!m_ok(M) || K < 1 || K > kMaxK || gate_rows < 0) return 0;
   if (M == 0) return BL_WS_HEADER_BYTES;
-  const int64_t blocks = bl::norm_grad_blocks(M);
+  const int64_t blocks = bl::norm_grad_blocks(M, K);
   const int64_t per = gate_rows > M ? M : gate_rows;
   const int64_t gates = per > 0 ? blocks + (M + per - 1) / per : 0;
   return BL_WS_HEADER_BYTES + round256(static_cast<size_t>(blocks) * 4 * K * sizeof(float)) +
@@ -609,7 +616,7 @@ bl_status bitlinear_residual_norm_backward(const bl_residual_norm_params* p, con
   const int64_t gate_rows = p->gate != nullptr ? (p->gate_rows > M ? M : p->gate_rows) : 0;
   const size_t need = bitlinear_residual_norm_backward_workspace_bytes(M, K, gate_rows);
   if (ws_bytes < need) return BL_ERR_WORKSPACE_TOO_SMALL;
-  const int64_t blocks = bl::norm_grad_blocks(M);
+  const int64_t blocks = bl::norm_grad_blocks(M, K);
   const int64_t gates = gate_rows > 0 ? blocks + (M + gate_rows - 1) / gate_rows : 0;
   uint8_t* s = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
   float* part = reinterpret_cast<float*>(s);

@@ -81,6 +81,31 @@ __device__ __forceinline__ void epilogue_store(const Epilogue& ep, void* y, int 
   store_out(y, ydt, o, v);
 }
 
+// act in place over NC values (fp32 bits): one unrolled loop per activation, the
+// choice is uniform and made once
+template <int NC>
+__device__ __forceinline__ void epilogue_act(int act, uint32_t (&acc)[NC]) {
+  switch (act) {
+    case BL_ACT_RELU:
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_apply(BL_ACT_RELU, __uint_as_float(acc[j])));
+      break;
+    case BL_ACT_RELU2:
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_apply(BL_ACT_RELU2, __uint_as_float(acc[j])));
+      break;
+    case BL_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_silu(__uint_as_float(acc[j])));
+      break;
+    case BL_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_gelu(__uint_as_float(acc[j])));
+      break;
+    default: break;
+  }
+}
+
 // NC outputs of one column n held as INT32 sums by a tensor-core epilogue
 // thread, for consecutive tokens: acc[j] becomes the bits of the fp32 output.
 // cf[j]: the tokens' dequantization factors; bias: the column's; o: the first
@@ -100,38 +125,13 @@ __device__ __forceinline__ void epilogue_chunk(const Epilogue& ep, uint32_t (&ac
 #pragma unroll
     for (int j = 0; j < NC; ++j) keep(j, __uint_as_float(acc[j]));
   }
-  // one unrolled loop per activation: the choice is uniform and made once
-  switch (ep.act) {
-    case BL_ACT_RELU:
-#pragma unroll
-      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_apply(BL_ACT_RELU, __uint_as_float(acc[j])));
-      break;
-    case BL_ACT_RELU2:
-#pragma unroll
-      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_apply(BL_ACT_RELU2, __uint_as_float(acc[j])));
-      break;
-    case BL_ACT_SILU:
-#pragma unroll
-      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_silu(__uint_as_float(acc[j])));
-      break;
-    case BL_ACT_GELU:
-#pragma unroll
-      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(act_gelu(__uint_as_float(acc[j])));
-      break;
-    default: break;
-  }
+  epilogue_act<NC>(ep.act, acc);
   if (ep.res != nullptr) {
-    if (live >= NC) {
-      float r[NC];
+    float r[NC];  // all loads in flight together
 #pragma unroll
-      for (int j = 0; j < NC; ++j) r[j] = load_out(ep.res, ydt, o + j * ld);
+    for (int j = 0; j < NC; ++j) r[j] = j < live ? load_out(ep.res, ydt, o + j * ld) : 0.0f;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(__fadd_rn(__uint_as_float(acc[j]), r[j]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < NC; ++j)
-        if (j < live) acc[j] = __float_as_uint(__fadd_rn(__uint_as_float(acc[j]), load_out(ep.res, ydt, o + j * ld)));
-    }
+    for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(__fadd_rn(__uint_as_float(acc[j]), r[j]));
   }
 }
 

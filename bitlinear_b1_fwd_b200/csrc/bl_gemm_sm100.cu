@@ -110,26 +110,6 @@ __device__ __forceinline__ void tmem_load<16>(uint32_t taddr, uint32_t (&r)[16])
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 16 two-bit digits (q + 1) -> 16 signed int8 weights q, in K order.  The
-// digits are spread into nibbles, which select bytes of 0x000100FF
-// (digit 0 -> 0xFF = -1, 1 -> 0, 2 -> +1, 3 -> 0).
-__device__ __forceinline__ uint32_t spread8(uint32_t h) {  // 8 digits in bits 0..15 -> 8 nibbles
-  uint32_t x = h & 0xffffu;
-  x = (x | (x << 8)) & 0x00ff00ffu;
-  x = (x | (x << 4)) & 0x0f0f0f0fu;
-  x = (x | (x << 2)) & 0x33333333u;
-  return x;
-}
-__device__ __forceinline__ uint4 expand16(uint32_t w) {
-  const uint32_t lo = spread8(w), hi = spread8(w >> 16);
-  uint4 o;
-  o.x = __byte_perm(0x000100ffu, 0u, lo & 0xffffu);
-  o.y = __byte_perm(0x000100ffu, 0u, lo >> 16);
-  o.z = __byte_perm(0x000100ffu, 0u, hi & 0xffffu);
-  o.w = __byte_perm(0x000100ffu, 0u, hi >> 16);
-  return o;
-}
-
 // One-SM tiles (5..128 tokens).  A work unit is a tile of 128 weight rows x BT
 // tokens over a range of k-blocks (128 K each): with ks > 1 the k-blocks of a
 // tile are cut into ks parts (units = tiles x ks, so that a small layer still
@@ -976,19 +956,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- host side --------------------------------------------------------------------
-bool encode_2d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stride,
-                  uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {stride};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Tensor map of y for the TMA-store epilogue: [M x N] of the output type, box
 // 128 rows x `tokens` tokens.  False when a row of y is not a multiple of 16
 // bytes.

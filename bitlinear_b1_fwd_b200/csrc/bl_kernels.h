@@ -81,6 +81,13 @@ cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const
                            int64_t ldx = 0);  // row stride of xq (a multiple of 16); 0: K
 cudaError_t launch_pad_codes(const int8_t* src, int64_t M, int64_t K, int64_t ld, int8_t* dst, cudaStream_t st);
 int gemm_split_k(int64_t M, int64_t N, int64_t K);
+// The product with an epilogue on weights expanded to int8 rows of ldw bytes.
+constexpr int64_t kGemmI8Tokens = 129;
+bool gemm_i8_fits(int64_t M, int64_t N, int ydt);
+cudaError_t launch_i2_to_i8(const uint8_t* i2, int64_t N, int64_t rowbytes, int8_t* w, cudaStream_t st);
+cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64_t ldw, const float* gamma,
+                           const float* scale, void* y, int ydt, int64_t M, int64_t N, int64_t K, const Epilogue& ep,
+                           void* ws, cudaStream_t st);
 cudaError_t launch_t5_to_i2(const uint8_t* t5, int64_t N, int64_t K, int64_t rb5, uint8_t* i2, int64_t rb2,
                             cudaStream_t st);
 // Output rows in up to kMaxRowGroups consecutive groups, each with its own
@@ -141,12 +148,12 @@ struct GradDwScratch {
 cudaError_t launch_grad_dw(const uint16_t* dz, const int8_t* xq, const float* scale, const float* gamma, int64_t M,
                            int64_t N, int64_t K, float* dw, const GradDwScratch& s, void* ws, cudaStream_t st);
 
-// The norms around a block's end.  Backward scratch: part [norm_grad_blocks(M)]
-// [4][K], gpart [norm_grad_blocks(M) + gate rows][K], stats [M][8] fp32.
+// The norms around a block's end.  Backward scratch: part [norm_grad_blocks(M, K)]
+// [4][K], gpart [norm_grad_blocks(M, K) + gate rows][K], stats [M][8] fp32.
 using NormParams = bl_residual_norm_params;
 cudaError_t launch_residual_norm(const NormParams& p, const void* b, int bdt, const void* r, int rdt, int64_t M,
                                  int64_t K, void* h, void* y, int ydt, int8_t* xq, float* scale, cudaStream_t st);
-int64_t norm_grad_blocks(int64_t M);
+int64_t norm_grad_blocks(int64_t M, int64_t K);
 cudaError_t launch_residual_norm_grad(const NormParams& p, const void* dy, int dydt, const void* dh, const void* b,
                                       int bdt, const void* h, int rdt, int64_t M, int64_t K, void* dr, void* db,
                                       float* dw1, float* db1, float* dgate, float* dw2, float* db2, float* part,

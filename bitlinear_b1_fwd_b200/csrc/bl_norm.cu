@@ -20,6 +20,8 @@
 // for the codes' maximum; backward two).  The column sums of the backward stay
 // in registers over a block's rows and meet in a second kernel in a fixed order.
 // Statistics are two-pass (the mean, then the squares about it) in fp32.
+#include <atomic>
+
 #include "bl_common.cuh"
 #include "bl_gemv.cuh"
 #include "bl_kernels.h"
@@ -30,9 +32,8 @@ namespace {
 
 // Threads of a block, by chunks and values per thread: what its registers allow.
 constexpr int norm_max_threads(int vec, int ni) { return vec == 8 && ni == 2 ? 576 : 512; }
-constexpr int grad_max_threads(int vec, int ni) { return vec == 8 && ni == 1 || ni == 4 ? 512 : 384; }
+constexpr int grad_max_threads(int vec, int ni) { return vec == 8 && ni == 1 || ni == 4 ? 512 : vec == 4 ? 1024 : 384; }
 constexpr int kNormLongThreads = 512;
-constexpr int kGradBlocks = 1;  // backward: blocks per SM
 constexpr size_t kGradSmemBudget = 225 * 1024;  // slots of the backward
 
 __device__ __forceinline__ NormParams params_after_wait(NormParams p) {
@@ -50,7 +51,7 @@ __device__ __forceinline__ void load_col(const float* p, int64_t k, float c, flo
   if (p == nullptr) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = c;
-  } else if ((reinterpret_cast<uintptr_t>(p + k) & 15) == 0 && VEC == 8) {
+  } else if (VEC > 1 && (reinterpret_cast<uintptr_t>(p + k) & 15) == 0) {
     load_vec<BL_F32, VEC>(p, k, v);
   } else {
 #pragma unroll
@@ -58,10 +59,10 @@ __device__ __forceinline__ void load_col(const float* p, int64_t k, float c, flo
   }
 }
 
-// 1 / sqrt of the mean square plus eps
-__device__ __forceinline__ float inv_dev(float sumsq, int64_t K, float eps) {
-  return __fdiv_rn(1.0f, __fsqrt_rn(sumsq / static_cast<float>(K) + eps));
-}
+// 1 / sqrt of the mean square plus eps.  Means are products with rk = 1 / K and
+// the root is rsqrtf (within 2 ulp): the IEEE divides and roots, in every thread
+// of a block for each row, were a quarter of the instructions.
+__device__ __forceinline__ float inv_dev(float sumsq, float rk, float eps) { return rsqrtf(fmaf(sumsq, rk, eps)); }
 
 // Column of value j of a thread's chunk i (VEC = 8: chunks of 8 neighbouring
 // columns; VEC = 1: neighbouring threads hold neighbouring columns).
@@ -77,71 +78,122 @@ template <int VEC, int NI>
 struct Slots {
   float* s;
   __device__ __forceinline__ void put(int v, int i, const float* x) {
-    if constexpr (VEC == 8) {
-      float4* q = reinterpret_cast<float4*>(s) + (v * NI + i) * 2 * blockDim.x + threadIdx.x;
-      q[0] = make_float4(x[0], x[1], x[2], x[3]);
-      q[blockDim.x] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
+    if constexpr (VEC == 1) {
       s[(v * NI + i) * blockDim.x + threadIdx.x] = x[0];
+    } else {
+      float4* q = reinterpret_cast<float4*>(s) + (v * NI + i) * (VEC / 4) * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int c = 0; c < VEC / 4; ++c) q[c * blockDim.x] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
     }
   }
-  __device__ __forceinline__ void get(int v, int i, float* x) const {
-    if constexpr (VEC == 8) {
-      const float4* q = reinterpret_cast<const float4*>(s) + (v * NI + i) * 2 * blockDim.x + threadIdx.x;
-      const float4 a = q[0], b = q[blockDim.x];
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  __device__ __forceinline__ void put(int v, int i, const Vals<VEC>& x) {
+    float f[VEC];
+    x.get(f);
+    put(v, i, f);
+  }
+  __device__ __forceinline__ Vals<VEC> get(int v, int i) const {
+    float f[VEC];
+    if constexpr (VEC == 1) {
+      f[0] = s[(v * NI + i) * blockDim.x + threadIdx.x];
     } else {
-      x[0] = s[(v * NI + i) * blockDim.x + threadIdx.x];
+      const float4* q = reinterpret_cast<const float4*>(s) + (v * NI + i) * (VEC / 4) * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int c = 0; c < VEC / 4; ++c) {
+        const float4 a = q[c * blockDim.x];
+        f[4 * c] = a.x; f[4 * c + 1] = a.y; f[4 * c + 2] = a.z; f[4 * c + 3] = a.w;
+      }
     }
+    Vals<VEC> r;
+    r.set(f);
+    return r;
   }
 };
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> col_vals(const float* p, int64_t k, float c) {
+  float f[VEC];
+  load_col<VEC>(p, k, c, f);
+  Vals<VEC> r;
+  r.set(f);
+  return r;
+}
 
 // bs gate w1 and bs gate b1: the branch's factor and offset, h = rs r + gw n1 + gb
 template <int VEC>
-__device__ __forceinline__ void branch_factor(const NormParams& p, const float* gate, int64_t k, float* gw) {
-  float g[VEC];
-  load_col<VEC>(gate, k, 1.0f, g);
-  load_col<VEC>(p.post_w, k, 1.0f, gw);
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) gw[j] = __fmul_rn(__fmul_rn(p.branch_scale, g[j]), gw[j]);
+__device__ __forceinline__ Vals<VEC> branch_factor(const NormParams& p, const float* gate, int64_t k) {
+  return mul(mul(splat<VEC>(p.branch_scale), col_vals<VEC>(gate, k, 1.0f)), col_vals<VEC>(p.post_w, k, 1.0f));
 }
 template <int VEC>
-__device__ __forceinline__ void branch_offset(const NormParams& p, const float* gate, int64_t k, float* gb) {
-  float g[VEC];
-  load_col<VEC>(gate, k, 1.0f, g);
-  load_col<VEC>(p.post_b, k, 0.0f, gb);
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) gb[j] = __fmul_rn(__fmul_rn(p.branch_scale, g[j]), gb[j]);
+__device__ __forceinline__ Vals<VEC> branch_offset(const NormParams& p, const float* gate, int64_t k) {
+  return mul(mul(splat<VEC>(p.branch_scale), col_vals<VEC>(gate, k, 1.0f)), col_vals<VEC>(p.post_b, k, 0.0f));
 }
 
-// Normalises the row held in v (zeros past K) in place; returns 1 / deviation.
 template <int VEC, int NI>
-__device__ __forceinline__ float normalise(float (&v)[NI][VEC], int kind, float eps, int64_t K, BlockSum& sum) {
-  if (kind == BL_NORM_NONE) return 1.0f;
-  if (kind == BL_NORM_LAYER) {
-    float s = 0.0f;
+__device__ __forceinline__ float sum_of(const Vals<VEC> (&v)[NI]) {
+  Vals<VEC> s = v[0];
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+  for (int i = 1; i < NI; ++i) s = add(s, v[i]);
+  return s.sum();
+}
+template <int VEC, int NI>
+__device__ __forceinline__ float dot_of(const Vals<VEC> (&v)[NI], const Vals<VEC> (&w)[NI]) {
+  Vals<VEC> s = mul(v[0], w[0]);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s += v[i][j];
-    const float mean = sum.one(s) / static_cast<float>(K);
+  for (int i = 1; i < NI; ++i) s = fma(v[i], w[i], s);
+  return s.sum();
+}
+
+// v - mean, zeros past K
+template <int VEC, int NI>
+__device__ __forceinline__ void centre(Vals<VEC> (&v)[NI], float mean, int64_t K) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = col0<VEC>(i) < K ? v[i][j] - mean : 0.0f;
+  for (int i = 0; i < NI; ++i) {
+    if (col0<VEC>(i) < K)
+      v[i] = add(v[i], splat<VEC>(-mean));
+    else
+      v[i].fill(0.0f);
   }
-  float q = 0.0f;
+}
+
+// Normalises the row held in v (zeros past K) in place.
+template <int VEC, int NI>
+__device__ __forceinline__ void normalise(Vals<VEC> (&v)[NI], int kind, float eps, int64_t K, float rk, BlockSum& sum) {
+  if (kind == BL_NORM_NONE) return;
+  if (kind == BL_NORM_LAYER) centre<VEC, NI>(v, __fmul_rn(sum.one(sum_of<VEC, NI>(v)), rk), K);
+  const Vals<VEC> r = splat<VEC>(inv_dev(sum.one(dot_of<VEC, NI>(v, v)), rk, eps));
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) v[i] = mul(v[i], r);
+}
+
+// The codes of eight values against s (c127 = fl(127 / s), |v| <= s) as bytes:
+// quant_act_fast_n with the codes taken from the low byte of t + 1.5 * 2^23 and
+// one test for all eight.
+__device__ __forceinline__ uint2 quant8(const Vals<8>& v, float s, float c127) {
+  const F2 c(c127, c127), magic(12582912.0f, 12582912.0f), back(-12582912.0f, -12582912.0f), minus(-1.0f, -1.0f);
+  uint32_t b[8];
+  float far = 0.0f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) q += v[i][j] * v[i][j];
-  const float r = inv_dev(sum.one(q), K, eps);
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) v[i][j] *= r;
-  return r;
+  for (int i = 0; i < 4; ++i) {
+    const F2 t = mul(v.p[i], c), r = add(t, magic), d = fma(add(r, back), minus, t);
+    float r0, r1, d0, d1;
+    r.get(r0, r1);
+    d.get(d0, d1);
+    b[2 * i] = __float_as_uint(r0);
+    b[2 * i + 1] = __float_as_uint(r1);
+    // NaN stays, and takes the branch below
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(fabsf(d0)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(fabsf(d1)));
+  }
+  if (!(far < 0.49993896484375f)) {
+    float f[8];
+    v.get(f);
+    int q[8];
+    quant_act_fast_n<8>(f, s, c127, q);
+    return make_uint2(pack4(q), pack4(q + 4));
+  }
+  auto four = [](const uint32_t* w) {
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  };
+  return make_uint2(four(b), four(b + 4));
 }
 
 // ---- forward, the row in registers --------------------------------------------
@@ -151,7 +203,7 @@ __device__ __forceinline__ float normalise(float (&v)[NI][VEC], int kind, float 
 constexpr bool norm_hold(int values) { return values <= 16; }
 
 template <int BDT, int RDT, int VEC, int NI, bool BIAS>
-__global__ void __launch_bounds__(norm_max_threads(VEC, NI))
+__global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC* NI == 8 ? 2 : 1)
     residual_norm_kernel(const NormParams p_arg, const void* __restrict__ b, const void* __restrict__ r, int64_t M,
                          int64_t K, void* __restrict__ h, void* __restrict__ y, int ydt, int8_t* __restrict__ xq,
                          float* __restrict__ scale) {
@@ -160,8 +212,8 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI))
   constexpr bool kHold = norm_hold(VEC * NI);
   extern __shared__ __align__(16) float slot_mem[];
   Slots<VEC, NI> slots{slot_mem};
-  __shared__ float4 buf[2][32];
-  BlockSum sum{buf, static_cast<int>(blockDim.x >> 5), 0};
+  __shared__ __align__(16) float sum_mem[2][4][32];
+  const float rk = __fdiv_rn(1.0f, static_cast<float>(K));
   Raw<BDT, VEC> nb[NI];
   Raw<RDT, VEC> nr[NI];
   auto fetch = [&](int64_t m) {
@@ -177,102 +229,77 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI))
       }
     }
   };
-  auto gate_row = [&](int64_t m) { return p.gate == nullptr ? nullptr : p.gate + (m / p.gate_rows) * K; };
-  auto hold_branch = [&](int64_t m) {
-    const float* gate = gate_row(m);
+  fetch(blockIdx.x);
+  // gate row of the block's current token, and the first token past it
+  int64_t g_row = p.gate == nullptr ? 0 : blockIdx.x / p.gate_rows, g_next = (g_row + 1) * p.gate_rows;
+  const float* gate = p.gate == nullptr ? nullptr : p.gate + g_row * K;
+  auto hold_branch = [&]() {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
       if (k < K) {
-        float t[VEC];
-        branch_factor<VEC>(p, gate, k, t);
-        slots.put(0, i, t);
-        if constexpr (BIAS) {
-          branch_offset<VEC>(p, gate, k, t);
-          slots.put(2, i, t);
-        }
+        slots.put(0, i, branch_factor<VEC>(p, gate, k));
+        if constexpr (BIAS) slots.put(2, i, branch_offset<VEC>(p, gate, k));
       }
     }
   };
-  fetch(blockIdx.x);
-  int64_t g_next = M;  // first token past the gate row held in the slots
   if constexpr (kHold) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
       if (k < K) {
-        float t[VEC];
-        load_col<VEC>(p.pre_w, k, 1.0f, t);
-        slots.put(1, i, t);
-        if constexpr (BIAS) {
-          load_col<VEC>(p.pre_b, k, 0.0f, t);
-          slots.put(3, i, t);
-        }
+        slots.put(1, i, col_vals<VEC>(p.pre_w, k, 1.0f));
+        if constexpr (BIAS) slots.put(3, i, col_vals<VEC>(p.pre_b, k, 0.0f));
       }
     }
-    hold_branch(blockIdx.x);
-    if (p.gate != nullptr) g_next = (blockIdx.x / p.gate_rows + 1) * p.gate_rows;
+    hold_branch();
   }
+  BlockSum sum(sum_mem);
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-    float v[NI][VEC], rr[NI][VEC];
+    Vals<VEC> v[NI], rr[NI];
     if constexpr (!kHold) {
       if (m != blockIdx.x) fetch(m);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      nb[i].get(v[i]);
-      nr[i].get(rr[i]);
+      v[i] = vals(nb[i]);
+      rr[i] = vals(nr[i]);
     }
-    if constexpr (kHold) {
-      fetch(m + gridDim.x);
-      if (m >= g_next) {
-        hold_branch(m);
-        g_next = (m / p.gate_rows + 1) * p.gate_rows;
-      }
+    if constexpr (kHold) fetch(m + gridDim.x);
+    if (p.gate != nullptr && m >= g_next) {
+      g_row = m / p.gate_rows;
+      g_next = (g_row + 1) * p.gate_rows;
+      gate = p.gate + g_row * K;
+      if constexpr (kHold) hold_branch();
     }
-    normalise<VEC, NI>(v, p.post, p.post_eps, K, sum);
+    normalise<VEC, NI>(v, p.post, p.post_eps, K, rk, sum);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
       if (k < K) {
-        float gw[VEC], gb[VEC];
-        if constexpr (kHold) {
-          slots.get(0, i, gw);
-          if constexpr (BIAS) slots.get(2, i, gb);
-        } else {
-          branch_factor<VEC>(p, gate_row(m), k, gw);
-          if constexpr (BIAS) branch_offset<VEC>(p, gate_row(m), k, gb);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          float t = p.res_scale * rr[i][j];
-          if constexpr (BIAS) t += gb[j];
-          v[i][j] = fmaf(gw[j], v[i][j], t);
-        }
-        if (h != nullptr) store_vec<RDT, VEC>(h, m * K + k, v[i]);
+        Vals<VEC> t = mul(rr[i], splat<VEC>(p.res_scale));
+        if constexpr (BIAS) t = add(t, kHold ? slots.get(2, i) : branch_offset<VEC>(p, gate, k));
+        v[i] = fma(kHold ? slots.get(0, i) : branch_factor<VEC>(p, gate, k), v[i], t);
+        if (h != nullptr) store_vals<RDT, VEC>(h, m * K + k, v[i]);
       }
     }
     if (y == nullptr && xq == nullptr) continue;
-    normalise<VEC, NI>(v, p.pre, p.pre_eps, K, sum);
+    normalise<VEC, NI>(v, p.pre, p.pre_eps, K, rk, sum);
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
       if (k < K) {
-        float w[VEC], c[VEC];
-        if constexpr (kHold) {
-          slots.get(1, i, w);
-          if constexpr (BIAS) slots.get(3, i, c);
-        } else {
-          load_col<VEC>(p.pre_w, k, 1.0f, w);
-          if constexpr (BIAS) load_col<VEC>(p.pre_b, k, 0.0f, c);
-        }
+        const Vals<VEC> w = kHold ? slots.get(1, i) : col_vals<VEC>(p.pre_w, k, 1.0f);
+        if constexpr (BIAS)
+          v[i] = fma(v[i], w, kHold ? slots.get(3, i) : col_vals<VEC>(p.pre_b, k, 0.0f));
+        else
+          v[i] = mul(v[i], w);
+        float f[VEC];
+        v[i].get(f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          v[i][j] = BIAS ? fmaf(v[i][j], w[j], c[j]) : __fmul_rn(v[i][j], w[j]);
-          amax = fmaxf(amax, fabsf(v[i][j]));
-        }
-        if (y != nullptr) store_vec_dt<VEC>(y, ydt, m * K + k, v[i]);
+        for (int j = 0; j < VEC; ++j) amax = fmaxf(amax, fabsf(f[j]));
+        if (y != nullptr) store_vec_dt<VEC>(y, ydt, m * K + k, f);
       }
     }
     if (xq == nullptr) continue;
@@ -282,12 +309,15 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI))
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
       if (k < K) {
-        int q[VEC];
-        quant_act_fast_n<VEC>(v[i], s, c127, q);
-        if constexpr (VEC == 8)
-          *reinterpret_cast<uint2*>(xq + m * K + k) = make_uint2(pack4(q), pack4(q + 4));
-        else
+        if constexpr (VEC == 8) {
+          *reinterpret_cast<uint2*>(xq + m * K + k) = quant8(v[i], s, c127);
+        } else {
+          float f[VEC];
+          int q[VEC];
+          v[i].get(f);
+          quant_act_fast_n<VEC>(f, s, c127, q);
           xq[m * K + k] = static_cast<int8_t>(q[0]);
+        }
       }
     }
     if (threadIdx.x == 0) scale[m] = s;
@@ -304,9 +334,9 @@ __global__ void __launch_bounds__(kNormLongThreads)
                               float* __restrict__ scale) {
   pdl_enter(b, r, h, y, xq, scale);
   const NormParams p = params_after_wait(p_arg);
-  __shared__ float4 buf[2][32];
-  BlockSum sum{buf, static_cast<int>(blockDim.x >> 5), 0};
-  const float fk = static_cast<float>(K);
+  __shared__ __align__(16) float sum_mem[2][4][32];
+  BlockSum sum(sum_mem);
+  const float rk = __fdiv_rn(1.0f, static_cast<float>(K));
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const float* gate = p.gate == nullptr ? nullptr : p.gate + (m / p.gate_rows) * K;
     float mean1 = 0.0f, r1 = 1.0f, mean2 = 0.0f, r2 = 1.0f;
@@ -333,13 +363,13 @@ __global__ void __launch_bounds__(kNormLongThreads)
       }
       return sum.one(s0 + s1);
     };
-    if (p.post == BL_NORM_LAYER) mean1 = total(bv) / fk;
+    if (p.post == BL_NORM_LAYER) mean1 = __fmul_rn(total(bv), rk);
     if (p.post != BL_NORM_NONE)
-      r1 = inv_dev(total([&](int64_t k) { const float d = bv(k) - mean1; return d * d; }), K, p.post_eps);
+      r1 = inv_dev(total([&](int64_t k) { const float d = bv(k) - mean1; return d * d; }), rk, p.post_eps);
     if (y != nullptr || xq != nullptr) {
-      if (p.pre == BL_NORM_LAYER) mean2 = total(hv) / fk;
+      if (p.pre == BL_NORM_LAYER) mean2 = __fmul_rn(total(hv), rk);
       if (p.pre != BL_NORM_NONE)
-        r2 = inv_dev(total([&](int64_t k) { const float d = hv(k) - mean2; return d * d; }), K, p.pre_eps);
+        r2 = inv_dev(total([&](int64_t k) { const float d = hv(k) - mean2; return d * d; }), rk, p.pre_eps);
     }
     float s = 1.0f, c127 = 127.0f;
     if (xq != nullptr) {
@@ -385,19 +415,18 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
                               float* __restrict__ part, float* __restrict__ gpart, float* __restrict__ dgate) {
   pdl_enter(dy, dh, b, h, dr, db, part, gpart, dgate);
   const NormParams p = params_after_wait(p_arg);
+  using V = Vals<VEC>;
   extern __shared__ __align__(16) float slot_mem[];
   Slots<VEC, NI> slots{slot_mem};
-  __shared__ float4 buf[2][32];
-  BlockSum sum{buf, static_cast<int>(blockDim.x >> 5), 0};
-  const float fk = static_cast<float>(K);
+  __shared__ __align__(16) float sum_mem[2][4][32];
+  const float rk = __fdiv_rn(1.0f, static_cast<float>(K));
   const int64_t m0 = blockIdx.x * rows_per, m1 = m0 + rows_per < M ? m0 + rows_per : M;
   constexpr bool kInReg = VEC * NI <= 8;
   constexpr int kRegs = kInReg ? NI : 1;
   constexpr int kAcc = 2;  // first slot of the running sums
   const int64_t plane = static_cast<int64_t>(gridDim.x) * K;
   bool grown = false;  // part holds dw1, db1 of earlier runs
-  float aw2[kRegs][VEC], aA[kRegs][VEC];
-  float ab2[BIAS ? kRegs : 1][VEC], aB[BIAS ? kRegs : 1][VEC];
+  V aw2[kRegs], aA[kRegs], ab2[BIAS ? kRegs : 1], aB[BIAS ? kRegs : 1];
   Raw<BDT, VEC> rb[NI];
   Raw<RDT, VEC> rh[NI], rg[NI];
   float gy[NI][VEC];
@@ -419,280 +448,178 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
       }
     }
   };
-  auto gate_row = [&](int64_t m) { return p.gate == nullptr ? nullptr : p.gate + (m / p.gate_rows) * K; };
-  auto hold_branch = [&](int64_t m) {
+  fetch(m0);
+  // gate row of the current run, and the first token past it
+  int64_t g_row = p.gate == nullptr ? 0 : m0 / p.gate_rows;
+  int64_t g_next = p.gate == nullptr ? M : (g_row + 1) * p.gate_rows;
+  auto gate = [&]() { return p.gate == nullptr ? nullptr : p.gate + g_row * K; };
+  auto hold_branch = [&]() {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
-      if (k < K) {
-        float t[VEC];
-        branch_factor<VEC>(p, gate_row(m), k, t);
-        slots.put(0, i, t);
-      }
+      if (k < K) slots.put(0, i, branch_factor<VEC>(p, gate(), k));
     }
   };
-  // the sums of a run that ends with token m: into dw1, db1 (slots) and its gate row
-  auto flush = [&](int64_t m) {
+  // the sums of a finished run: into dw1, db1 and its gate row
+  auto flush = [&]() {
+    const bool whole = gate_row_whole(g_row, p.gate_rows, M, m0, m1);
+    float* dst = dgate == nullptr ? nullptr : whole ? dgate + g_row * K : gpart + (blockIdx.x + g_row) * K;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
       if (k < K) {
-        float g[VEC], w[VEC], c[VEC], t[VEC];
-        float sA[VEC], sB[VEC];
-        const float zero[VEC] = {};
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          sA[j] = aA[kInReg ? i : 0][j];
-          sB[j] = BIAS ? aB[BIAS && kInReg ? i : 0][j] : 0.0f;
-        }
-        if constexpr (!kInReg) {
-          slots.get(kAcc + 1, i, sA);
-          slots.put(kAcc + 1, i, zero);
+        V sA, sB;
+        if constexpr (kInReg) {
+          sA = aA[i];
+          aA[i].fill(0.0f);
           if constexpr (BIAS) {
-            slots.get(kAcc + 3, i, sB);
-            slots.put(kAcc + 3, i, zero);
+            sB = aB[i];
+            aB[i].fill(0.0f);
+          }
+        } else {
+          sA = slots.get(kAcc + 1, i);
+          slots.put(kAcc + 1, i, splat<VEC>(0.0f));
+          if constexpr (BIAS) {
+            sB = slots.get(kAcc + 3, i);
+            slots.put(kAcc + 3, i, splat<VEC>(0.0f));
           }
         }
-        load_col<VEC>(gate_row(m), k, 1.0f, g);
-        auto grow = [&](int slot, int vec, const float* a) {
-          float* at = kInReg || part == nullptr ? nullptr : part + vec * plane + blockIdx.x * K + k;
+        const V bg = mul(splat<VEC>(p.branch_scale), col_vals<VEC>(gate(), k, 1.0f));
+        auto grow = [&](int slot, int vec, const V& a) {
           if constexpr (kInReg) {
-            slots.get(slot, i, t);
-          } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) t[j] = 0.0f;
-            if (grown && at != nullptr) load_vec<BL_F32, VEC>(at, 0, t);
+            slots.put(slot, i, fma(bg, a, slots.get(slot, i)));
+          } else if (part != nullptr) {
+            float* at = part + vec * plane + blockIdx.x * K;
+            store_vals<BL_F32, VEC>(at, k, fma(bg, a, grown ? col_vals<VEC>(at, k, 0.0f) : splat<VEC>(0.0f)));
           }
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) t[j] = fmaf(__fmul_rn(p.branch_scale, g[j]), a[j], t[j]);
-          if constexpr (kInReg)
-            slots.put(slot, i, t);
-          else if (at != nullptr)
-            store_vec<BL_F32, VEC>(at, 0, t);
         };
         grow(2, 2, sA);
         if constexpr (BIAS) grow(3, 3, sB);
-        if (dgate != nullptr) {
-          load_col<VEC>(p.post_w, k, 1.0f, w);
-          if constexpr (BIAS) load_col<VEC>(p.post_b, k, 0.0f, c);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            t[j] = __fmul_rn(w[j], sA[j]);
-            if constexpr (BIAS) t[j] = fmaf(c[j], sB[j], t[j]);
-            t[j] = __fmul_rn(p.branch_scale, t[j]);
-          }
-          const int64_t row = m / p.gate_rows;
-          const bool whole = gate_row_whole(row, p.gate_rows, M, m0, m1);
-          float* dst = whole ? dgate + row * K + k : gpart + (blockIdx.x + row) * K + k;
-          if (VEC == 8 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-            store_vec<BL_F32, VEC>(dst, 0, t);
+        if (dst != nullptr) {
+          V t = mul(col_vals<VEC>(p.post_w, k, 1.0f), sA);
+          if constexpr (BIAS) t = fma(col_vals<VEC>(p.post_b, k, 0.0f), sB, t);
+          t = mul(splat<VEC>(p.branch_scale), t);
+          if (VEC > 1 && (reinterpret_cast<uintptr_t>(dst + k) & 15) == 0) {
+            store_vals<BL_F32, VEC>(dst, k, t);
           } else {
+            float f[VEC];
+            t.get(f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) dst[j] = t[j];
+            for (int j = 0; j < VEC; ++j) dst[k + j] = f[j];
           }
-        }
-      }
-      if constexpr (kInReg) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          aA[i][j] = 0.0f;
-          if constexpr (BIAS) aB[i][j] = 0.0f;
         }
       }
     }
     grown = true;
   };
-  fetch(m0);
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int64_t k = col0<VEC>(i);
-    const float zero[VEC] = {};
 #pragma unroll
-    for (int v = 2; v < grad_slots(VEC * NI, BIAS); ++v) slots.put(v, i, zero);
+    for (int v = 2; v < grad_slots(VEC * NI, BIAS); ++v) slots.put(v, i, splat<VEC>(0.0f));
     if constexpr (kInReg) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        aw2[i][j] = aA[i][j] = 0.0f;
-        if constexpr (BIAS) ab2[i][j] = aB[i][j] = 0.0f;
+      aw2[i].fill(0.0f);
+      aA[i].fill(0.0f);
+      if constexpr (BIAS) {
+        ab2[i].fill(0.0f);
+        aB[i].fill(0.0f);
       }
     }
-    if (k < K) {
-      float t[VEC];
-      load_col<VEC>(p.pre_w, k, 1.0f, t);
-      slots.put(1, i, t);
-    }
+    if (k < K) slots.put(1, i, col_vals<VEC>(p.pre_w, k, 1.0f));
   }
-  hold_branch(m0);
-  int64_t g_next = p.gate == nullptr ? M : (m0 / p.gate_rows + 1) * p.gate_rows;
+  hold_branch();
+  BlockSum sum(sum_mem);
   for (int64_t m = m0; m < m1; ++m) {
-    float n1[NI][VEC], n2[NI][VEC], d2[NI][VEC], d[NI][VEC], dyv[NI][VEC];
+    V n1[NI], n2[NI], d2[NI], d[NI], dyv[NI];
     if constexpr (!kInReg) {
       if (m != m0) fetch(m);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      rb[i].get(n1[i]);
-      rh[i].get(n2[i]);
-      rg[i].get(d[i]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) dyv[i][j] = gy[i][j];
+      n1[i] = vals(rb[i]);
+      n2[i] = vals(rh[i]);
+      d[i] = vals(rg[i]);
+      dyv[i].set(gy[i]);
     }
     if constexpr (kInReg) fetch(m + 1);
     if (m >= g_next) {
-      flush(m - 1);
-      hold_branch(m);
+      flush();
+      ++g_row;
       g_next += p.gate_rows;
+      hold_branch();
     }
     if (p.post == BL_NORM_LAYER || p.pre == BL_NORM_LAYER) {
-      float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          s1 += n1[i][j];
-          s2 += n2[i][j];
-        }
-      const float2 t = sum.two(s1, s2);
-      const float mean1 = p.post == BL_NORM_LAYER ? t.x / fk : 0.0f;
-      const float mean2 = p.pre == BL_NORM_LAYER ? t.y / fk : 0.0f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          n1[i][j] = col0<VEC>(i) < K ? n1[i][j] - mean1 : 0.0f;
-          n2[i][j] = col0<VEC>(i) < K ? n2[i][j] - mean2 : 0.0f;
-        }
+      const float2 t = sum.two(sum_of<VEC, NI>(n1), sum_of<VEC, NI>(n2));
+      if (p.post == BL_NORM_LAYER) centre<VEC, NI>(n1, __fmul_rn(t.x, rk), K);
+      if (p.pre == BL_NORM_LAYER) centre<VEC, NI>(n2, __fmul_rn(t.y, rk), K);
     }
     // both deviations, and the sums through the norm before the next block
-    float q1 = 0.0f, q2 = 0.0f, sd = 0.0f, sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      float w[VEC];
-      if (k < K) slots.get(1, i, w);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        d2[i][j] = k < K ? __fmul_rn(dyv[i][j], w[j]) : 0.0f;
-        q1 = fmaf(n1[i][j], n1[i][j], q1);
-        q2 = fmaf(n2[i][j], n2[i][j], q2);
-        sd += d2[i][j];
-        sq = fmaf(d2[i][j], n2[i][j], sq);
-      }
+      if (col0<VEC>(i) < K)
+        d2[i] = mul(dyv[i], slots.get(1, i));
+      else
+        d2[i].fill(0.0f);
     }
-    const float4 t = sum.four(q1, q2, sd, sq);
-    const float r1 = p.post == BL_NORM_NONE ? 1.0f : inv_dev(t.x, K, p.post_eps);
-    const float r2 = p.pre == BL_NORM_NONE ? 1.0f : inv_dev(t.y, K, p.pre_eps);
-    const float s = p.pre == BL_NORM_LAYER ? t.z / fk : 0.0f;
-    const float q = p.pre == BL_NORM_NONE ? 0.0f : __fmul_rn(r2, t.w) / fk;
-    float s1 = 0.0f, p1 = 0.0f;
+    const float4 t = sum.four(dot_of<VEC, NI>(n1, n1), dot_of<VEC, NI>(n2, n2), sum_of<VEC, NI>(d2),
+                              dot_of<VEC, NI>(d2, n2));
+    const float r1 = p.post == BL_NORM_NONE ? 1.0f : inv_dev(t.x, rk, p.post_eps);
+    const float r2 = p.pre == BL_NORM_NONE ? 1.0f : inv_dev(t.y, rk, p.pre_eps);
+    const float s = p.pre == BL_NORM_LAYER ? __fmul_rn(t.z, rk) : 0.0f;
+    const float q = p.pre == BL_NORM_NONE ? 0.0f : __fmul_rn(__fmul_rn(r2, t.w), rk);
+    const V r1v = splat<VEC>(r1), r2v = splat<VEC>(r2), mq = splat<VEC>(-q), ms = splat<VEC>(-s);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t k = col0<VEC>(i);
+      n1[i] = mul(n1[i], r1v);
       if (k < K) {
-        float gw[VEC], out[VEC];
-        slots.get(0, i, gw);
-        float sw2[VEC], sA[VEC], sb2[VEC], sB[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          sw2[j] = aw2[kInReg ? i : 0][j];
-          sA[j] = aA[kInReg ? i : 0][j];
-          sb2[j] = ab2[BIAS && kInReg ? i : 0][j];
-          sB[j] = aB[BIAS && kInReg ? i : 0][j];
-        }
-        if constexpr (!kInReg) {
-          slots.get(kAcc, i, sw2);
-          slots.get(kAcc + 1, i, sA);
-          if constexpr (BIAS) {
-            slots.get(kAcc + 2, i, sb2);
-            slots.get(kAcc + 3, i, sB);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float u2 = __fmul_rn(n2[i][j], r2);
-          n1[i][j] = __fmul_rn(n1[i][j], r1);
-          d[i][j] = fmaf(r2, fmaf(-u2, q, __fsub_rn(d2[i][j], s)), d[i][j]);
-          out[j] = __fmul_rn(p.res_scale, d[i][j]);
-          sw2[j] = fmaf(dyv[i][j], u2, sw2[j]);
-          sA[j] = fmaf(d[i][j], n1[i][j], sA[j]);
-          if constexpr (BIAS) {
-            sb2[j] += dyv[i][j];
-            sB[j] += d[i][j];
-          }
-          d2[i][j] = __fmul_rn(gw[j], d[i][j]);  // dn1
-          s1 += d2[i][j];
-          p1 = fmaf(d2[i][j], n1[i][j], p1);
-        }
+        const V u2 = mul(n2[i], r2v);
+        d[i] = fma(r2v, fma(u2, mq, add(d2[i], ms)), d[i]);
+        if (dr != nullptr) store_vals<RDT, VEC>(dr, m * K + k, mul(splat<VEC>(p.res_scale), d[i]));
         if constexpr (kInReg) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            aw2[i][j] = sw2[j];
-            aA[i][j] = sA[j];
-            if constexpr (BIAS) {
-              ab2[i][j] = sb2[j];
-              aB[i][j] = sB[j];
-            }
+          aw2[i] = fma(dyv[i], u2, aw2[i]);
+          aA[i] = fma(d[i], n1[i], aA[i]);
+          if constexpr (BIAS) {
+            ab2[i] = add(ab2[i], dyv[i]);
+            aB[i] = add(aB[i], d[i]);
           }
         } else {
-          slots.put(kAcc, i, sw2);
-          slots.put(kAcc + 1, i, sA);
+          slots.put(kAcc, i, fma(dyv[i], u2, slots.get(kAcc, i)));
+          slots.put(kAcc + 1, i, fma(d[i], n1[i], slots.get(kAcc + 1, i)));
           if constexpr (BIAS) {
-            slots.put(kAcc + 2, i, sb2);
-            slots.put(kAcc + 3, i, sB);
+            slots.put(kAcc + 2, i, add(slots.get(kAcc + 2, i), dyv[i]));
+            slots.put(kAcc + 3, i, add(slots.get(kAcc + 3, i), d[i]));
           }
         }
-        if (dr != nullptr) store_vec<RDT, VEC>(dr, m * K + k, out);
-      }
+        d2[i] = mul(slots.get(0, i), d[i]);  // dn1
+      }  // (d2 and n1 are zeros past K)
     }
     if (db != nullptr) {
-      if (p.post == BL_NORM_NONE) {
-        s1 = p1 = 0.0f;
-      } else {
-        const float2 t1 = sum.two(s1, p1);
-        s1 = p.post == BL_NORM_LAYER ? t1.x / fk : 0.0f;
-        p1 = t1.y / fk;
+      float s1 = 0.0f, p1 = 0.0f;
+      if (p.post != BL_NORM_NONE) {
+        const float2 t1 = sum.two(sum_of<VEC, NI>(d2), dot_of<VEC, NI>(d2, n1));
+        s1 = p.post == BL_NORM_LAYER ? __fmul_rn(t1.x, rk) : 0.0f;
+        p1 = __fmul_rn(t1.y, rk);
       }
+      const V mp = splat<VEC>(-p1), m1v = splat<VEC>(-s1);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int64_t k = col0<VEC>(i);
-        if (k < K) {
-          float out[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            out[j] = __fmul_rn(r1, fmaf(-n1[i][j], p1, __fsub_rn(d2[i][j], s1)));
-          store_vec<BDT, VEC>(db, m * K + k, out);
-        }
+        if (k < K) store_vals<BDT, VEC>(db, m * K + k, mul(r1v, fma(n1[i], mp, add(d2[i], m1v))));
       }
     }
   }
-  flush(m1 - 1);
+  flush();
   if (part == nullptr) return;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int64_t k = col0<VEC>(i), o = static_cast<int64_t>(blockIdx.x) * K + k;
     if (k < K) {
-      float t[VEC];
-      auto sums = [&](const float* in_reg, int slot) {
-        if constexpr (kInReg) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) t[j] = in_reg[j];
-        } else {
-          slots.get(slot, i, t);
-        }
-      };
-      sums(aw2[kInReg ? i : 0], kAcc);
-      store_vec<BL_F32, VEC>(part, o, t);
-      if constexpr (BIAS) {
-        sums(ab2[BIAS && kInReg ? i : 0], kAcc + 2);
-        store_vec<BL_F32, VEC>(part, o + plane, t);
-      }
+      store_vals<BL_F32, VEC>(part, o, kInReg ? aw2[kInReg ? i : 0] : slots.get(kAcc, i));
+      if constexpr (BIAS) store_vals<BL_F32, VEC>(part, o + plane, kInReg ? ab2[kInReg ? i : 0] : slots.get(kAcc + 2, i));
       if constexpr (kInReg) {
-        slots.get(2, i, t);
-        store_vec<BL_F32, VEC>(part, o + 2 * plane, t);
-        if constexpr (BIAS) {
-          slots.get(3, i, t);
-          store_vec<BL_F32, VEC>(part, o + 3 * plane, t);
-        }
+        store_vals<BL_F32, VEC>(part, o + 2 * plane, slots.get(2, i));
+        if constexpr (BIAS) store_vals<BL_F32, VEC>(part, o + 3 * plane, slots.get(3, i));
       }
     }
   }
@@ -730,9 +657,9 @@ __global__ void __launch_bounds__(kNormLongThreads)
                                     const void* __restrict__ h, int64_t M, int64_t K, GradRow* __restrict__ stats) {
   pdl_enter(dy, dh, b, h, stats);
   const NormParams p = params_after_wait(p_arg);
-  __shared__ float4 buf[2][32];
-  BlockSum sum{buf, static_cast<int>(blockDim.x >> 5), 0};
-  const float fk = static_cast<float>(K);
+  __shared__ __align__(16) float sum_mem[2][4][32];
+  BlockSum sum(sum_mem);
+  const float rk = __fdiv_rn(1.0f, static_cast<float>(K));
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const float* gate = p.gate == nullptr ? nullptr : p.gate + (m / p.gate_rows) * K;
     GradRow t{0.0f, 1.0f, 0.0f, 1.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -747,16 +674,16 @@ __global__ void __launch_bounds__(kNormLongThreads)
       a += bv(k);
       c += hv(k);
     });
-    if (p.post == BL_NORM_LAYER) t.mean1 = mean.x / fk;
-    if (p.pre == BL_NORM_LAYER) t.mean2 = mean.y / fk;
+    if (p.post == BL_NORM_LAYER) t.mean1 = __fmul_rn(mean.x, rk);
+    if (p.pre == BL_NORM_LAYER) t.mean2 = __fmul_rn(mean.y, rk);
     const float2 sq = total([&](int64_t k, float& a, float& c) {
       const float d1 = bv(k) - t.mean1, d2 = hv(k) - t.mean2;
       a += d1 * d1;
       c += d2 * d2;
     });
-    if (p.post != BL_NORM_NONE) t.r1 = inv_dev(sq.x, K, p.post_eps);
+    if (p.post != BL_NORM_NONE) t.r1 = inv_dev(sq.x, rk, p.post_eps);
     if (p.pre != BL_NORM_NONE) {
-      t.r2 = inv_dev(sq.y, K, p.pre_eps);
+      t.r2 = inv_dev(sq.y, rk, p.pre_eps);
       const float2 v = total([&](int64_t k, float& a, float& c) {
         float g, w2;
         load_vec_dt<1>(dy, dydt, m * K + k, &g);
@@ -764,8 +691,8 @@ __global__ void __launch_bounds__(kNormLongThreads)
         a += g * w2;
         c += g * w2 * (hv(k) - t.mean2) * t.r2;
       });
-      t.s = p.pre == BL_NORM_LAYER ? v.x / fk : 0.0f;
-      t.q = v.y / fk;
+      t.s = p.pre == BL_NORM_LAYER ? __fmul_rn(v.x, rk) : 0.0f;
+      t.q = __fmul_rn(v.y, rk);
     }
     if (p.post != BL_NORM_NONE) {
       const float2 v = total([&](int64_t k, float& a, float& c) {
@@ -777,8 +704,8 @@ __global__ void __launch_bounds__(kNormLongThreads)
         a += dn1;
         c += dn1 * e.n1;
       });
-      t.s1 = p.post == BL_NORM_LAYER ? v.x / fk : 0.0f;
-      t.q1 = v.y / fk;
+      t.s1 = p.post == BL_NORM_LAYER ? __fmul_rn(v.x, rk) : 0.0f;
+      t.q1 = __fmul_rn(v.y, rk);
     }
     if (threadIdx.x == 0) stats[m] = t;
   }
@@ -888,19 +815,26 @@ int row_threads(int64_t K, int vec, int ni) {
   return static_cast<int>(((K + per - 1) / per + 31) / 32 * 32);
 }
 
-// Blocks that stay on an SM: some 1280 threads (the register form's 48 or so
-// registers per thread; more blocks only add turns of the column vectors).
-unsigned resident_grid(int threads, int64_t rows) {
-  const int64_t per = 1280 / threads, cap = device_sms() * (per < 1 ? 1 : (per > 16 ? 16 : per));
-  return static_cast<unsigned>(rows < cap ? rows : cap);
-}
-
 // Dynamic shared memory above the 48 KB that need no opt-in.
 template <typename Kern>
 cudaError_t allow_smem(Kern kern, size_t bytes) {
   return bytes <= 48 * 1024 ? cudaSuccess
                             : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(bytes));
+}
+
+// The grid of a persistent kernel for `rows` work items: one wave.  `memo` keeps
+// the blocks per SM of each block size (they depend on nothing else).
+template <typename Kern>
+unsigned one_wave(Kern kern, std::atomic<int>* memo, int threads, size_t smem, int64_t rows) {
+  int per_sm = memo[threads / 32].load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1)
+      per_sm = 1;
+    memo[threads / 32].store(per_sm, std::memory_order_relaxed);
+  }
+  const int64_t cap = static_cast<int64_t>(device_sms()) * per_sm;
+  return static_cast<unsigned>(rows < cap ? rows : cap);
 }
 
 template <int BDT, int RDT, int VEC, int NI>
@@ -912,7 +846,8 @@ cudaError_t launch_fwd_row(const NormParams& p, const void* b, const void* r, in
   const size_t smem = norm_hold(VEC * NI) ? static_cast<size_t>(bias ? 4 : 2) * t * VEC * NI * sizeof(float) : 0;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, resident_grid(t, M), t, smem, st, p, b, r, M, K, h, y, ydt, xq, scale);
+  static std::atomic<int> memo[2][33];
+  return launch_pdl(kern, one_wave(kern, memo[bias], t, smem, M), t, smem, st, p, b, r, M, K, h, y, ydt, xq, scale);
 }
 
 template <int BDT, int RDT>
@@ -932,7 +867,8 @@ cudaError_t launch_fwd(const NormParams& p, const void* b, const void* r, int64_
   }
 #undef BL_NF
   auto kern = residual_norm_long_kernel<BDT, RDT>;
-  return launch_pdl(kern, resident_grid(kNormLongThreads, M), kNormLongThreads, 0, st, p, b, r, M, K, h, y, ydt, xq,
+  static std::atomic<int> memo[33];
+  return launch_pdl(kern, one_wave(kern, memo, kNormLongThreads, 0, M), kNormLongThreads, 0, st, p, b, r, M, K, h, y, ydt, xq,
                     scale);
 }
 
@@ -974,7 +910,8 @@ cudaError_t launch_bwd(const NormParams& p, const void* dy, int dydt, const void
 #undef BL_NB
   GradRow* rows = static_cast<GradRow*>(stats);
   auto ks = residual_norm_grad_stats_kernel<BDT, RDT>;
-  cudaError_t e = launch_pdl(ks, resident_grid(kNormLongThreads, M), kNormLongThreads, 0, st, p, dy, dydt, dh, b, h, M,
+  static std::atomic<int> memo[33];
+  cudaError_t e = launch_pdl(ks, one_wave(ks, memo, kNormLongThreads, 0, M), kNormLongThreads, 0, st, p, dy, dydt, dh, b, h, M,
                              K, rows);
   if (e != cudaSuccess) return e;
   return launch_pdl(residual_norm_grad_cols_kernel<BDT, RDT>,
@@ -986,9 +923,12 @@ cudaError_t launch_bwd(const NormParams& p, const void* dy, int dydt, const void
 
 }  // namespace
 
-// Row blocks of the backward (partial sums): kGradBlocks per SM.
-int64_t norm_grad_blocks(int64_t M) {
-  const int64_t most = kGradBlocks * device_sms();
+// Row blocks of the backward (partial sums): what fits the SMs at some 832
+// threads each (64 registers a thread), eight blocks per SM at most.
+int64_t norm_grad_blocks(int64_t M, int64_t K) {
+  int64_t per_sm = 832 / row_threads(K, 4, 1);
+  per_sm = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
+  const int64_t most = per_sm * device_sms();
   const int64_t rows_per = (M + most - 1) / most;
   return rows_per > 0 ? (M + rows_per - 1) / rows_per : 1;
 }
@@ -1009,7 +949,7 @@ cudaError_t launch_residual_norm_grad(const NormParams& p, const void* dy, int d
                                       int bdt, const void* h, int rdt, int64_t M, int64_t K, void* dr, void* db,
                                       float* dw1, float* db1, float* dgate, float* dw2, float* db2, float* part,
                                       float* gpart, void* stats, cudaStream_t st) {
-  const int64_t blocks = norm_grad_blocks(M);
+  const int64_t blocks = norm_grad_blocks(M, K);
   const int64_t rows_per = (M + blocks - 1) / blocks;
   const bool sums = db1 != nullptr || db2 != nullptr;
   const bool bias = sums || (dgate != nullptr && p.post_b != nullptr);  // dgate takes sum dh with a bias

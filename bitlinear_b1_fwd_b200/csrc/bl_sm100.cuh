@@ -127,6 +127,50 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// ---- tcgen05 --------------------------------------------------------------------
+// arrive on the barrier at this offset in each CTA of `mask` when the MMAs issued
+// so far complete
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 16 columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// 16 two-bit digits (q + 1) -> 16 signed int8 weights q, in K order.  The
+// digits are spread into nibbles, which select bytes of 0x000100FF
+// (digit 0 -> 0xFF = -1, 1 -> 0, 2 -> +1, 3 -> 0).
+__device__ __forceinline__ uint32_t spread8(uint32_t h) {  // 8 digits in bits 0..15 -> 8 nibbles
+  uint32_t x = h & 0xffffu;
+  x = (x | (x << 8)) & 0x00ff00ffu;
+  x = (x | (x << 4)) & 0x0f0f0f0fu;
+  x = (x | (x << 2)) & 0x33333333u;
+  return x;
+}
+__device__ __forceinline__ uint4 expand16(uint32_t w) {
+  const uint32_t lo = spread8(w), hi = spread8(w >> 16);
+  uint4 o;
+  o.x = __byte_perm(0x000100ffu, 0u, lo & 0xffffu);
+  o.y = __byte_perm(0x000100ffu, 0u, lo >> 16);
+  o.z = __byte_perm(0x000100ffu, 0u, hi & 0xffffu);
+  o.w = __byte_perm(0x000100ffu, 0u, hi >> 16);
+  return o;
+}
+
 // ---- bulk copies (no tensor map) and bulk-group waits --------------------------------
 // global -> shared, completion counted on an mbarrier (size: a multiple of 16 B,
 // both addresses 16-byte aligned)

@@ -5,19 +5,6 @@
 
 namespace bl {
 
-// VEC consecutive elements from element e (VEC = 8: e a multiple of 8 and the
-// array 16-byte aligned; VEC = 1: any), widened to fp32.
-template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const void* p, int64_t e, float* v) {
-  if constexpr (VEC == 8) {
-    float t[8];
-    load8_aligned<DT>(p, e, t);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = t[j];
-  } else {
-    v[0] = load_elem<DT>(p, e);
-  }
-}
 // VEC consecutive elements as loaded, widened when they are used.
 template <int DT, int VEC>
 struct Raw;
@@ -51,6 +38,31 @@ struct Raw<BL_F32, 8> {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 };
+template <>
+struct Raw<BL_BF16, 4> {
+  uint2 q;
+  __device__ __forceinline__ void zero() { q = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    q = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + e));
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = __uint_as_float(q.x << 16);
+    v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16);
+    v[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+};
+template <>
+struct Raw<BL_F32, 4> {
+  float4 a;
+  __device__ __forceinline__ void zero() { a = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + e));
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+};
 template <int DT>
 struct Raw<DT, 1> {
   float f;
@@ -59,6 +71,23 @@ struct Raw<DT, 1> {
   __device__ __forceinline__ void get(float* v) const { v[0] = f; }
 };
 
+// VEC consecutive elements from element e (VEC = 8, 4: e a multiple of it and
+// the array 16-byte aligned; VEC = 1: any), widened to fp32.
+template <int DT, int VEC>
+__device__ __forceinline__ void load_vec(const void* p, int64_t e, float* v) {
+  if constexpr (VEC == 8) {
+    float t[8];
+    load8_aligned<DT>(p, e, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = t[j];
+  } else if constexpr (VEC == 4) {
+    Raw<DT, 4> r;
+    r.load(p, e);
+    r.get(v);
+  } else {
+    v[0] = load_elem<DT>(p, e);
+  }
+}
 template <int VEC>
 __device__ __forceinline__ void load_vec_dt(const void* p, int dt, int64_t e, float* v) {
   if (dt == BL_F32)
@@ -79,6 +108,8 @@ __device__ __forceinline__ void store_vec(void* p, int64_t e, const float* v) {
     if constexpr (VEC == 8) {
       reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(q)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (VEC == 4) {
+      reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
     } else {
       q[0] = v[0];
     }
@@ -86,6 +117,8 @@ __device__ __forceinline__ void store_vec(void* p, int64_t e, const float* v) {
     if constexpr (VEC == 8) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e) =
           make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+    } else if constexpr (VEC == 4) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + e) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     } else {
       static_cast<__nv_bfloat16*>(p)[e] = __float2bfloat16_rn(v[0]);
     }
@@ -99,61 +132,201 @@ __device__ __forceinline__ void store_vec_dt(void* p, int dt, int64_t e, const f
     store_vec<BL_BF16, VEC>(p, e, v);
 }
 
-// Sums of one to four values over the block in a fixed order, the same in every
-// thread; one barrier.  Two buffers alternate: a buffer is written again only
-// after the barrier of the next sum, which every thread reaches after its
+// ---- packed fp32 pairs ----------------------------------------------------------
+// add, mul and fma on two fp32 values in one instruction, each value rounded as
+// the scalar instruction rounds it.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  }
+};
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
+// VEC neighbouring values as pairs (VEC = 1: one value).
+template <int VEC>
+struct Vals {
+  static constexpr int P = VEC / 2;
+  F2 p[P];
+  __device__ __forceinline__ void fill(float c) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = F2(c, c);
+  }
+  __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = F2(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i].get(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ float sum() const {
+    F2 s = p[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) s = add(s, p[i]);
+    float a, b;
+    s.get(a, b);
+    return a + b;
+  }
+};
+template <>
+struct Vals<1> {
+  float f0;
+  __device__ __forceinline__ void fill(float c) { f0 = c; }
+  __device__ __forceinline__ void set(const float* f) { f0 = f[0]; }
+  __device__ __forceinline__ void get(float* f) const { f[0] = f0; }
+  __device__ __forceinline__ float sum() const { return f0; }
+};
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> splat(float c) {
+  Vals<VEC> r;
+  r.fill(c);
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> add(const Vals<VEC>& a, const Vals<VEC>& b) {
+  Vals<VEC> r;
+  if constexpr (VEC == 1) {
+    r.f0 = __fadd_rn(a.f0, b.f0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.p[i] = add(a.p[i], b.p[i]);
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> mul(const Vals<VEC>& a, const Vals<VEC>& b) {
+  Vals<VEC> r;
+  if constexpr (VEC == 1) {
+    r.f0 = __fmul_rn(a.f0, b.f0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.p[i] = mul(a.p[i], b.p[i]);
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> fma(const Vals<VEC>& a, const Vals<VEC>& b, const Vals<VEC>& c) {
+  Vals<VEC> r;
+  if constexpr (VEC == 1) {
+    r.f0 = __fmaf_rn(a.f0, b.f0, c.f0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.p[i] = fma(a.p[i], b.p[i], c.p[i]);
+  }
+  return r;
+}
+template <int DT, int VEC>
+__device__ __forceinline__ Vals<VEC> vals(const Raw<DT, VEC>& r) {
+  float f[VEC];
+  r.get(f);
+  Vals<VEC> v;
+  v.set(f);
+  return v;
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void store_vals(void* p, int64_t e, const Vals<VEC>& v) {
+  float f[VEC];
+  v.get(f);
+  store_vec<DT, VEC>(p, e, f);
+}
+
+// Sums of one, two or four values over the block in a fixed order, the same in
+// every thread; one barrier.  Within a warp two and four values share the
+// exchanges: each step halves the values a lane carries, then the lanes (six
+// shuffles for four values).  After the barrier one load per lane takes in every
+// warp's sums (16 or 8 bytes: neighbouring warps), and the same exchanges over
+// the lanes of a value finish.  Two buffers alternate: a buffer is written again
+// only after the barrier of the next sum, which every thread reaches after its
 // reads.
 struct BlockSum {
-  float4 (*buf)[32];  // shared [2][32]
+  float (*buf)[4][32];  // shared [2][4][32]: phase, value, warp; zero past the last warp
   int nw, phase;
-  template <int N>
-  __device__ __forceinline__ void run(float (&a)[N]) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < N; ++j) a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
-    if (nw == 1) return;
-    float4* w = buf[phase];
-    phase ^= 1;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) {
-      float* d = reinterpret_cast<float*>(w + (threadIdx.x >> 5));
-#pragma unroll
-      for (int j = 0; j < N; ++j) d[j] = a[j];
+  __device__ __forceinline__ BlockSum(float (*b)[4][32]) : buf(b), nw(static_cast<int>(blockDim.x >> 5)), phase(0) {
+    if (nw > 1) {
+      for (int i = threadIdx.x; i < 2 * 4 * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.0f;
+      __syncthreads();
     }
-    __syncthreads();
-    const float* d = reinterpret_cast<const float*>(w + lane);
+  }
+  template <int FROM>
+  static __device__ __forceinline__ float lanes(float a) {  // over groups of 2 FROM lanes
 #pragma unroll
-    for (int j = 0; j < N; ++j) a[j] = lane < nw ? d[j] : 0.0f;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < N; ++j) a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
+    for (int o = FROM; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+  }
+  static __device__ __forceinline__ float sum4(const float* w) {
+    const float4 q = *reinterpret_cast<const float4*>(w);
+    return (q.x + q.y) + (q.z + q.w);
   }
   __device__ __forceinline__ float one(float a) {
-    float v[1] = {a};
-    run(v);
-    return v[0];
-  }
-  __device__ __forceinline__ float2 two(float a, float b) {
-    float v[2] = {a, b};
-    run(v);
-    return make_float2(v[0], v[1]);
-  }
-  __device__ __forceinline__ float4 four(float a, float b, float c, float d) {
-    float v[4] = {a, b, c, d};
-    run(v);
-    return make_float4(v[0], v[1], v[2], v[3]);
-  }
-  __device__ __forceinline__ float max(float a) {
-    a = warp_maxf(a);
+    a = lanes<16>(a);
     if (nw == 1) return a;
-    float4* w = buf[phase];
+    float (*w)[32] = buf[phase];
     phase ^= 1;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) w[threadIdx.x >> 5].x = a;
+    if (lane == 0) w[0][threadIdx.x >> 5] = a;
     __syncthreads();
-    return warp_maxf(lane < nw ? w[lane].x : 0.0f);
+    return lanes<4>(sum4(w[0] + 4 * (lane & 7)));
+  }
+  __device__ __forceinline__ float2 two(float a, float b) {
+    const int lane = threadIdx.x & 31;
+    const bool up = (lane & 16) != 0;
+    a = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);  // lanes 0-15: a, 16-31: b
+    a = lanes<8>(a);
+    if (nw > 1) {
+      float (*w)[32] = buf[phase];
+      phase ^= 1;
+      if ((lane & 15) == 0) w[lane >> 4][threadIdx.x >> 5] = a;
+      __syncthreads();
+      const float2 q = *reinterpret_cast<const float2*>(w[lane >> 4] + 2 * (lane & 15));
+      a = lanes<8>(q.x + q.y);
+    }
+    return make_float2(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 16));
+  }
+  __device__ __forceinline__ float4 four(float a, float b, float c, float d) {
+    const int lane = threadIdx.x & 31;
+    const bool up = (lane & 16) != 0, odd = (lane & 8) != 0;
+    a = (up ? c : a) + __shfl_xor_sync(0xffffffffu, up ? a : c, 16);  // lanes 0-15: a, b, 16-31: c, d
+    b = (up ? d : b) + __shfl_xor_sync(0xffffffffu, up ? b : d, 16);
+    a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);  // eight lanes each
+    a = lanes<4>(a);
+    if (nw > 1) {
+      float (*w)[32] = buf[phase];
+      phase ^= 1;
+      if ((lane & 7) == 0) w[lane >> 3][threadIdx.x >> 5] = a;
+      __syncthreads();
+      a = lanes<4>(sum4(w[lane >> 3] + 4 * (lane & 7)));
+    }
+    return make_float4(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 8),
+                       __shfl_sync(0xffffffffu, a, 16), __shfl_sync(0xffffffffu, a, 24));
+  }
+  // the largest of non-negative values (their bits order like unsigned integers)
+  __device__ __forceinline__ float max(float a) {
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+    if (nw == 1) return __uint_as_float(m);
+    float (*w)[32] = buf[phase];
+    phase ^= 1;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) w[0][threadIdx.x >> 5] = __uint_as_float(m);
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, lane < nw ? __float_as_uint(w[0][lane]) : 0u);
+    return __uint_as_float(m);
   }
 };
 
