@@ -21,7 +21,9 @@ namespace {
 constexpr int kAgCols = 32, kAgRows = 8;  // threads of a block along columns and rows
 constexpr int kAgResident = 4;            // blocks that fit an SM together (64 registers a thread)
 // rows a thread has in flight: what its 64 registers hold
-constexpr int ag_unroll(int dyt, int zt, int vec) { return vec == 8 && (dyt == BL_F32 || zt == BL_F32) ? 2 : 4; }
+constexpr int ag_unroll(int dyt, int zt, int vec) {
+  return vec == 1 ? 8 : dyt == BL_F32 || zt == BL_F32 ? 2 : 4;
+}
 
 // act'(z).  For bf16 gradients the fast exponential and divide: their errors
 // (below 2^-20 for |z| < 30) are far under half a bf16 step, 2^-9.
@@ -33,10 +35,14 @@ __device__ __forceinline__ float act_slope(float z) {
     const float s = FAST ? __fdividef(1.0f, 1.0f + __expf(-z)) : __fdiv_rn(1.0f, 1.0f + expf(-z));
     return s * (1.0f + z * (1.0f - s));
   }
-  if constexpr (ACT == BL_ACT_GELU) {
-    const float t = -0.5f * z * z;
-    const float pdf = 0.39894228040143268f * (FAST ? __expf(t) : expf(t));
-    return 0.5f * erfcf(-0.70710678118654752f * z) + z * pdf;
+  if constexpr (ACT == BL_ACT_GELU) {  // Phi(z) + z phi(z)
+    if constexpr (FAST) {
+      float e;
+      const float tail = normal_tail(z, &e);
+      return fmaf(z, 0.39894228040143268f * e, z < 0.0f ? tail : 1.0f - tail);
+    } else {
+      return 0.5f * erfcf(-0.70710678118654752f * z) + z * (0.39894228040143268f * expf(-0.5f * z * z));
+    }
   }
   return 1.0f;
 }

@@ -213,6 +213,13 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
   if (!aligned(packed, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(scale, 4) ||
       !aligned(gamma, 4) || !aligned(ws, 16))
     return BL_ERR_MISALIGNED;
+  if (ep.act >= 0 && bl::gemm_few_fits(M, N, K)) {
+    const int64_t rb = bitlinear_packed_row_bytes(K, fmt);
+    if (ws_bytes < BL_WS_HEADER_BYTES + bl::gemm_few_bytes(M, rb, fmt)) return BL_ERR_WORKSPACE_TOO_SMALL;
+    return cuda_status(bl::launch_gemm_few(packed, fmt, rb, gamma, N, K, x, xdt, scale, M, y, ydt, ep,
+                                           static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES,
+                                           static_cast<cudaStream_t>(stream)));
+  }
   const bool pad = ep.act >= 0 && pads_codes(M, K);
   const bool many = ep.act >= 0 && M >= bl::kGemmI8Tokens;
   if (ws_bytes < forward_bytes(M, N, K, fmt, xdt, pad, many)) return BL_ERR_WORKSPACE_TOO_SMALL;
@@ -269,6 +276,9 @@ bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, 
 }
 
 size_t bitlinear_forward_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
+  if (!m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
+  if (bl::gemm_few_fits(M, N, K))
+    return BL_WS_HEADER_BYTES + bl::gemm_few_bytes(M, bitlinear_packed_row_bytes(K, fmt), fmt);
   return forward_bytes(M, N, K, fmt, xdt, pads_codes(M, K), M >= bl::kGemmI8Tokens);
 }
 

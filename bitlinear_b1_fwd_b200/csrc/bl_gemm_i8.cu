@@ -280,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         };
         if (ep.pre != nullptr) put(kBox);
-        epilogue_act<NC>(ep.act, v);
+        epilogue_act<NC, YDT == BL_BF16>(ep.act, v);
         if (ep.res != nullptr) {
           if (!wait_warp(resf + e, res_phase, limit, abort_flag)) {
             if (lane == 0) {

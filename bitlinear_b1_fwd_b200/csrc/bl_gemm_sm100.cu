@@ -859,22 +859,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
 // the same weight), for the tensor-core path.  Item (n, t): the 16 base-3
 // bytes 16t .. 16t + 15 of row n (weights 80t .. 80t + 79; bytes past rb5 read
 // as padding, 121 = five weight-0 digits) become 160 bits, i.e. five 32-bit
-// words at byte 20t of the 2-bit row (words past rb2 are dropped).  With
-// q_i = floor(b / 3^i) the digits of b are d_i = q_i - 3 q_{i+1}, so its ten bits
-// are sum d_i 4^i = b + q_1 + 4 q_2 + 16 q_3 + 64 q_4: four divisions by 3 (the
-// multiply by 171 / 512, exact below 256), two bytes at a time in the 16-bit
-// halves of a register.  No table: the 32 KB one per block that this replaces
+// words at byte 20t of the 2-bit row (words past rb2 are dropped).
+// No table: the 32 KB one per block that this replaces
 // took longer to fill than a 3200 x 8640 matrix takes to transcode.
-__device__ __forceinline__ uint32_t t5_pair(uint32_t x) {  // two bytes at bits 0 and 16 -> two 10-bit fields there
-  const uint32_t over = ((x + 0x000d000du) >> 8 & 0x00010001u) * 0xffu;  // bytes 243..255: five weight-0 digits (121)
-  x = (x & ~over) | (0x00790079u & over);
-  const uint32_t q1 = (x * 171u >> 9) & 0x007f007fu;
-  const uint32_t q2 = (q1 * 171u >> 9) & 0x007f007fu;
-  const uint32_t q3 = (q2 * 171u >> 9) & 0x007f007fu;
-  const uint32_t q4 = (q3 * 171u >> 9) & 0x007f007fu;
-  return x + q1 + 4u * q2 + 16u * q3 + 64u * q4;
-}
-
 __global__ void __launch_bounds__(256)
     t5_to_i2_kernel(const uint8_t* __restrict__ t5, int64_t N, int64_t K, int64_t rb5, uint8_t* __restrict__ i2,
                     int64_t rb2) {
@@ -889,19 +876,8 @@ __global__ void __launch_bounds__(256)
     const int64_t n = nn;
     const uint4 v = 16 * static_cast<int64_t>(t) < rb5 ? __ldcg(reinterpret_cast<const uint4*>(t5 + n * rb5 + 16 * t))
                                  : make_uint4(0x79797979u, 0x79797979u, 0x79797979u, 0x79797979u);
-    const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-    uint64_t f[4];  // 40 bits of each packed word
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = t5_pair(wd[i] & 0x00ff00ffu), c = t5_pair((wd[i] >> 8) & 0x00ff00ffu);  // bytes 0, 2 and 1, 3
-      const uint32_t lo = (a & 0x3ffu) | (c & 0x3ffu) << 10, hi = a >> 16 | (c >> 16) << 10;
-      f[i] = static_cast<uint64_t>(lo) | static_cast<uint64_t>(hi) << 20;
-    }
-    const uint32_t out[5] = {static_cast<uint32_t>(f[0]),
-                             static_cast<uint32_t>(f[0] >> 32) | static_cast<uint32_t>(f[1]) << 8,
-                             static_cast<uint32_t>(f[1] >> 24) | static_cast<uint32_t>(f[2]) << 16,
-                             static_cast<uint32_t>(f[2] >> 16) | static_cast<uint32_t>(f[3]) << 24,
-                             static_cast<uint32_t>(f[3] >> 8)};
+    uint32_t out[5];
+    t5_segment(v, out);
     uint32_t* dst = reinterpret_cast<uint32_t*>(i2 + n * rb2) + 5 * t;
 #pragma unroll
     for (int j = 0; j < 5; ++j)

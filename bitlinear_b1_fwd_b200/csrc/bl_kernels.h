@@ -88,6 +88,14 @@ cudaError_t launch_i2_to_i8(const uint8_t* i2, int64_t N, int64_t rowbytes, int8
 cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64_t ldw, const float* gamma,
                            const float* scale, void* y, int ydt, int64_t M, int64_t N, int64_t K, const Epilogue& ep,
                            void* ws, cudaStream_t st);
+// The product with an epilogue of a few tokens, from packed weights; scratch of
+// gemm_few_bytes for the tokens' codes.
+constexpr int64_t kFewCodeBytes = int64_t{48} << 20;
+bool gemm_few_fits(int64_t M, int64_t N, int64_t K);
+size_t gemm_few_bytes(int64_t M, int64_t rowbytes, int fmt);
+cudaError_t launch_gemm_few(const uint8_t* packed, int fmt, int64_t rowbytes, const float* gamma, int64_t N, int64_t K,
+                            const void* x, int xdt, float* scale, int64_t M, void* y, int ydt, const Epilogue& ep,
+                            void* scratch, cudaStream_t st);
 cudaError_t launch_t5_to_i2(const uint8_t* t5, int64_t N, int64_t K, int64_t rb5, uint8_t* i2, int64_t rb2,
                             cudaStream_t st);
 // Output rows in up to kMaxRowGroups consecutive groups, each with its own

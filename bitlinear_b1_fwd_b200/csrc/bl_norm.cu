@@ -203,7 +203,7 @@ __device__ __forceinline__ uint2 quant8(const Vals<8>& v, float s, float c127) {
 constexpr bool norm_hold(int values) { return values <= 16; }
 
 template <int BDT, int RDT, int VEC, int NI, bool BIAS>
-__global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC* NI == 8 ? 2 : 1)
+__global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC * NI <= 8 ? 2 : 1)
     residual_norm_kernel(const NormParams p_arg, const void* __restrict__ b, const void* __restrict__ r, int64_t M,
                          int64_t K, void* __restrict__ h, void* __restrict__ y, int ydt, int8_t* __restrict__ xq,
                          float* __restrict__ scale) {
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
   V aw2[kRegs], aA[kRegs], ab2[BIAS ? kRegs : 1], aB[BIAS ? kRegs : 1];
   Raw<BDT, VEC> rb[NI];
   Raw<RDT, VEC> rh[NI], rg[NI];
-  float gy[NI][VEC];
+  RawAny<VEC> gy[NI];
   auto fetch = [&](int64_t m) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -438,13 +438,12 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
       if (m < m1 && k < K) {
         rb[i].load(b, m * K + k);
         rh[i].load(h, m * K + k);
-        load_vec_dt<VEC>(dy, dydt, m * K + k, gy[i]);
+        gy[i].load(dy, dydt, m * K + k);
         if (dh != nullptr) rg[i].load(dh, m * K + k);
       } else {
         rb[i].zero();
         rh[i].zero();
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) gy[i][j] = 0.0f;
+        gy[i].zero(dydt);
       }
     }
   };
@@ -539,7 +538,9 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
       n1[i] = vals(rb[i]);
       n2[i] = vals(rh[i]);
       d[i] = vals(rg[i]);
-      dyv[i].set(gy[i]);
+      float f[VEC];
+      gy[i].get(dydt, f);
+      dyv[i].set(f);
     }
     if constexpr (kInReg) fetch(m + 1);
     if (m >= g_next) {

@@ -171,6 +171,36 @@ __device__ __forceinline__ uint4 expand16(uint32_t w) {
   return o;
 }
 
+// A base-3 segment (16 bytes, 80 weights) as five words of 2-bit codes (a base-3
+// digit is the 2-bit code of the same weight).  With q_i = floor(b / 3^i) the
+// digits of a byte b are d_i = q_i - 3 q_{i+1}, so its ten bits are sum d_i 4^i =
+// b + q_1 + 4 q_2 + 16 q_3 + 64 q_4: four divisions by 3 (the multiply by 171 /
+// 512, exact below 256), two bytes at a time in the 16-bit halves of a register.
+__device__ __forceinline__ uint32_t t5_pair(uint32_t x) {  // two bytes at bits 0 and 16 -> two 10-bit fields there
+  const uint32_t over = ((x + 0x000d000du) >> 8 & 0x00010001u) * 0xffu;  // bytes 243..255: five weight-0 digits (121)
+  x = (x & ~over) | (0x00790079u & over);
+  const uint32_t q1 = (x * 171u >> 9) & 0x007f007fu;
+  const uint32_t q2 = (q1 * 171u >> 9) & 0x007f007fu;
+  const uint32_t q3 = (q2 * 171u >> 9) & 0x007f007fu;
+  const uint32_t q4 = (q3 * 171u >> 9) & 0x007f007fu;
+  return x + q1 + 4u * q2 + 16u * q3 + 64u * q4;
+}
+__device__ __forceinline__ void t5_segment(const uint4& v, uint32_t* out) {
+  const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+  uint64_t f[4];  // 40 bits of each packed word
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = t5_pair(wd[i] & 0x00ff00ffu), c = t5_pair((wd[i] >> 8) & 0x00ff00ffu);  // bytes 0, 2 and 1, 3
+    const uint32_t lo = (a & 0x3ffu) | (c & 0x3ffu) << 10, hi = a >> 16 | (c >> 16) << 10;
+    f[i] = static_cast<uint64_t>(lo) | static_cast<uint64_t>(hi) << 20;
+  }
+  out[0] = static_cast<uint32_t>(f[0]);
+  out[1] = static_cast<uint32_t>(f[0] >> 32) | static_cast<uint32_t>(f[1]) << 8;
+  out[2] = static_cast<uint32_t>(f[1] >> 24) | static_cast<uint32_t>(f[2]) << 16;
+  out[3] = static_cast<uint32_t>(f[2] >> 16) | static_cast<uint32_t>(f[3]) << 24;
+  out[4] = static_cast<uint32_t>(f[3] >> 8);
+}
+
 // ---- bulk copies (no tensor map) and bulk-group waits --------------------------------
 // global -> shared, completion counted on an mbarrier (size: a multiple of 16 B,
 // both addresses 16-byte aligned)

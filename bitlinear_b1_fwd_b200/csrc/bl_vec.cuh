@@ -63,12 +63,29 @@ struct Raw<BL_F32, 4> {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   }
 };
-template <int DT>
-struct Raw<DT, 1> {
+template <>
+struct Raw<BL_F32, 1> {
   float f;
   __device__ __forceinline__ void zero() { f = 0.0f; }
-  __device__ __forceinline__ void load(const void* p, int64_t e) { f = load_elem<DT>(p, e); }
+  __device__ __forceinline__ void load(const void* p, int64_t e) { f = __ldcg(static_cast<const float*>(p) + e); }
   __device__ __forceinline__ void get(float* v) const { v[0] = f; }
+};
+template <>
+struct Raw<BL_BF16, 1> {
+  uint16_t q;
+  __device__ __forceinline__ void zero() { q = 0; }
+  __device__ __forceinline__ void load(const void* p, int64_t e) { q = __ldcg(static_cast<const uint16_t*>(p) + e); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = bf16_bits_to_f32(q); }
+};
+
+// The same of a type known at run time.
+template <int VEC>
+struct RawAny {
+  Raw<BL_BF16, VEC> h;
+  Raw<BL_F32, VEC> f;
+  __device__ __forceinline__ void zero(int dt) { dt == BL_F32 ? f.zero() : h.zero(); }
+  __device__ __forceinline__ void load(const void* p, int dt, int64_t e) { dt == BL_F32 ? f.load(p, e) : h.load(p, e); }
+  __device__ __forceinline__ void get(int dt, float* v) const { dt == BL_F32 ? f.get(v) : h.get(v); }
 };
 
 // VEC consecutive elements from element e (VEC = 8, 4: e a multiple of it and
