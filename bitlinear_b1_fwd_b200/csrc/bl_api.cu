@@ -76,30 +76,18 @@ bool uses_gemm(int64_t M, int64_t K) { return M > bl::kGemvMaxTokens && (K % 16)
 // transcoded to 2 bits in the workspace for the decode path too.
 bool b1_via_i2(int fmt, int64_t K) { return fmt == BL_PACK_B1 && (K + 7) / 8 > 4096; }
 
-// With an epilogue, batches of more than kGemvMaxTokens tokens whose K is no
-// multiple of 16 take the tensor cores too, on a padded copy of the codes (37
-// tokens, 1011 -> 777: 419 us as ten decode products, 26 us so).
-inline bool pads_codes(int64_t M, int64_t K) { return M > bl::kGemvMaxTokens && K % 16 != 0; }
-inline int64_t padded_codes(int64_t K) { return (K + 15) / 16 * 16; }
-
-static size_t forward_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt, bool pad, bool i8) {
+size_t bitlinear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
   if (!m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
   size_t bytes = BL_WS_HEADER_BYTES;
-  if (pad || uses_gemm(M, K)) {
+  if (uses_gemm(M, K)) {
     if (xdt != BL_I8) bytes += round256(static_cast<size_t>(M * K));
-    if (pad) bytes += round256(static_cast<size_t>(M * padded_codes(K)));
     if (fmt != BL_PACK_I2) bytes += round256(static_cast<size_t>(N * bitlinear_packed_row_bytes(K, BL_PACK_I2)));
-    if (i8) bytes += round256(static_cast<size_t>(N * 4 * bitlinear_packed_row_bytes(K, BL_PACK_I2)));
     const int ks = bl::gemm_split_k(M, N, K);
     if (ks > 1) bytes += round256(static_cast<size_t>(ks) * M * N * sizeof(int32_t));
   } else if (b1_via_i2(fmt, K)) {
     bytes += round256(static_cast<size_t>(N * bitlinear_packed_row_bytes(K, BL_PACK_I2)));
   }
   return bytes;
-}
-
-size_t bitlinear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
-  return forward_bytes(M, N, K, fmt, xdt, false, false);
 }
 
 bl_status bitlinear_workspace_init(void* ws, size_t ws_bytes, void* stream) {
@@ -200,9 +188,9 @@ bl_status bitlinear_layernorm_quantize_acts(const void* x, int xdt, const float*
   return cuda_status(bl::launch_ln_quant(x, xdt, ln_w, ln_b, eps, M, K, y, xq, scale, static_cast<cudaStream_t>(stream)));
 }
 
-static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K, const void* x,
-                              int xdt, float* scale, int64_t M, void* y, int ydt, const bl::Epilogue& ep, void* ws,
-                              size_t ws_bytes, void* stream) {
+bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
+                            const void* x, int xdt, float* scale, int64_t M, void* y, int ydt, void* ws,
+                            size_t ws_bytes, void* stream) {
   if (!fmt_ok(fmt) || !(float_dt(xdt) || xdt == BL_I8) || !(float_dt(ydt) || ydt == BL_I32))
     return BL_ERR_INVALID_VALUE;
   if (!m_ok(M) || !nk_ok(N, K)) return BL_ERR_INVALID_VALUE;
@@ -213,18 +201,9 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
   if (!aligned(packed, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(scale, 4) ||
       !aligned(gamma, 4) || !aligned(ws, 16))
     return BL_ERR_MISALIGNED;
-  if (ep.act >= 0 && bl::gemm_few_fits(M, N, K)) {
-    const int64_t rb = bitlinear_packed_row_bytes(K, fmt);
-    if (ws_bytes < BL_WS_HEADER_BYTES + bl::gemm_few_bytes(M, rb, fmt)) return BL_ERR_WORKSPACE_TOO_SMALL;
-    return cuda_status(bl::launch_gemm_few(packed, fmt, rb, gamma, N, K, x, xdt, scale, M, y, ydt, ep,
-                                           static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES,
-                                           static_cast<cudaStream_t>(stream)));
-  }
-  const bool pad = ep.act >= 0 && pads_codes(M, K);
-  const bool many = ep.act >= 0 && M >= bl::kGemmI8Tokens;
-  if (ws_bytes < forward_bytes(M, N, K, fmt, xdt, pad, many)) return BL_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < bitlinear_forward_workspace_bytes(M, N, K, fmt, xdt)) return BL_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!pad && !uses_gemm(M, K)) {
+  if (!uses_gemm(M, K)) {
     if (b1_via_i2(fmt, K)) {
       uint8_t* w2 = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
       const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
@@ -234,7 +213,8 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
       fmt = BL_PACK_I2;
     }
     if (bl::gemv_max_tokens(fmt, bitlinear_packed_row_bytes(K, fmt)) < 1) return BL_ERR_UNSUPPORTED;
-    return cuda_status(bl::launch_gemv(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::one_group(N, ep), ws, st));
+    return cuda_status(bl::launch_gemv(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt,
+                                       bl::one_group(N, bl::no_epilogue()), ws, st));
   }
   uint8_t* scratch = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
   const int8_t* xq = static_cast<const int8_t*>(x);
@@ -243,12 +223,6 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
       return BL_ERR_CUDA;
     xq = reinterpret_cast<const int8_t*>(scratch);
     scratch += round256(static_cast<size_t>(M * K));
-  }
-  if (pad) {
-    int8_t* padded = reinterpret_cast<int8_t*>(scratch);
-    if (bl::launch_pad_codes(xq, M, K, padded_codes(K), padded, st) != cudaSuccess) return BL_ERR_CUDA;
-    xq = padded;
-    scratch += round256(static_cast<size_t>(M * padded_codes(K)));
   }
   const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
   const uint8_t* w2 = packed;
@@ -260,37 +234,91 @@ static bl_status forward_with(const uint8_t* packed, int fmt, const float* gamma
     w2 = scratch;
     scratch += round256(static_cast<size_t>(N * rb2));
   }
-  if (many && bl::gemm_i8_fits(M, N, ydt)) {
-    int8_t* w8 = reinterpret_cast<int8_t*>(scratch);
-    if (bl::launch_i2_to_i8(w2, N, rb2, w8, st) != cudaSuccess) return BL_ERR_CUDA;
-    return cuda_status(bl::launch_gemm_i8(xq, padded_codes(K), w8, 4 * rb2, gamma, scale, y, ydt, M, N, K, ep, ws, st));
-  }
   int32_t* part = bl::gemm_split_k(M, N, K) > 1 ? reinterpret_cast<int32_t*>(scratch) : nullptr;
-  return cuda_status(bl::launch_gemm_i2(xq, w2, rb2, gamma, scale, y, ydt, M, N, K, N, part, ws, 0, 0, st, ep, padded_codes(K)));
+  return cuda_status(bl::launch_gemm_i2(xq, w2, rb2, gamma, scale, y, ydt, M, N, K, N, part, ws, 0, 0, st));
 }
 
-bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
-                            const void* x, int xdt, float* scale, int64_t M, void* y, int ydt, void* ws,
-                            size_t ws_bytes, void* stream) {
-  return forward_with(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::no_epilogue(), ws, ws_bytes, stream);
+// The product with its epilogue: the decode kernels for one token, a kernel on
+// packed weights for a few, the product of int8 weights for more.
+enum class ForwardPath { kGemv, kFew, kMany };
+static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K) {
+  return M <= bl::kEpilogueGemvTokens ? ForwardPath::kGemv
+         : bl::gemm_few_fits(M, N, K) ? ForwardPath::kFew
+                                      : ForwardPath::kMany;
 }
+static int64_t padded_codes(int64_t K) { return (K + 15) / 16 * 16; }  // TMA rows
 
 size_t bitlinear_forward_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
   if (!m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
-  if (bl::gemm_few_fits(M, N, K))
-    return BL_WS_HEADER_BYTES + bl::gemm_few_bytes(M, bitlinear_packed_row_bytes(K, fmt), fmt);
-  return forward_bytes(M, N, K, fmt, xdt, pads_codes(M, K), M >= bl::kGemmI8Tokens);
+  const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
+  size_t bytes = BL_WS_HEADER_BYTES;
+  switch (epilogue_path(M, N, K)) {
+    case ForwardPath::kGemv:
+      if (b1_via_i2(fmt, K)) bytes += round256(static_cast<size_t>(N * rb2));
+      return bytes;
+    case ForwardPath::kFew: return bytes + bl::gemm_few_bytes(M, bitlinear_packed_row_bytes(K, fmt), fmt);
+    default: break;
+  }
+  if (xdt != BL_I8) bytes += round256(static_cast<size_t>(M * K));
+  if (K % 16 != 0) bytes += round256(static_cast<size_t>(M * padded_codes(K)));
+  if (fmt != BL_PACK_I2) bytes += round256(static_cast<size_t>(N * rb2));
+  return bytes + round256(static_cast<size_t>(N * 4 * rb2));
 }
 
 bl_status bitlinear_forward_epilogue(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
                                      const void* x, int xdt, float* scale, int64_t M, const float* bias, int act,
                                      const void* residual, void* preact, void* y, int ydt, void* ws, size_t ws_bytes,
                                      void* stream) {
-  if (!float_dt(ydt) || !act_ok(act)) return BL_ERR_INVALID_VALUE;
+  if (!fmt_ok(fmt) || !(float_dt(xdt) || xdt == BL_I8) || !float_dt(ydt) || !act_ok(act)) return BL_ERR_INVALID_VALUE;
   if (preact != nullptr && (preact == y || preact == residual)) return BL_ERR_INVALID_VALUE;
   if (!aligned(bias, 4) || !aligned(residual, 16) || !aligned(preact, 16)) return BL_ERR_MISALIGNED;
-  return forward_with(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::Epilogue{bias, residual, preact, act}, ws,
-                      ws_bytes, stream);
+  if (!m_ok(M) || !nk_ok(N, K)) return BL_ERR_INVALID_VALUE;
+  if (M == 0 || N == 0) return BL_OK;
+  if (packed == nullptr || gamma == nullptr || x == nullptr || scale == nullptr || y == nullptr || ws == nullptr)
+    return BL_ERR_INVALID_VALUE;
+  if (!aligned(packed, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(scale, 4) || !aligned(gamma, 4) ||
+      !aligned(ws, 16))
+    return BL_ERR_MISALIGNED;
+  if (ws_bytes < bitlinear_forward_epilogue_workspace_bytes(M, N, K, fmt, xdt)) return BL_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* scratch = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
+  const int64_t rb = bitlinear_packed_row_bytes(K, fmt), rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
+  const bl::Epilogue ep{bias, residual, preact, act};
+  const ForwardPath path = epilogue_path(M, N, K);
+  if (path == ForwardPath::kFew)
+    return cuda_status(bl::launch_gemm_few(packed, fmt, rb, gamma, N, K, x, xdt, scale, M, y, ydt, ep, scratch, st));
+  if (path == ForwardPath::kGemv) {
+    if (b1_via_i2(fmt, K)) {
+      if (bl::launch_b1_to_i2(packed, N, K, rb, scratch, rb2, st) != cudaSuccess) return BL_ERR_CUDA;
+      packed = scratch;
+      fmt = BL_PACK_I2;
+    }
+    if (bl::gemv_max_tokens(fmt, bitlinear_packed_row_bytes(K, fmt)) < 1) return BL_ERR_UNSUPPORTED;
+    return cuda_status(bl::launch_gemv(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::one_group(N, ep), ws, st));
+  }
+  const int8_t* xq = static_cast<const int8_t*>(x);
+  if (xdt != BL_I8) {
+    int8_t* codes = reinterpret_cast<int8_t*>(scratch);
+    if (bl::launch_act_quant(x, xdt, M, K, codes, scale, st) != cudaSuccess) return BL_ERR_CUDA;
+    xq = codes;
+    scratch += round256(static_cast<size_t>(M * K));
+  }
+  if (K % 16 != 0) {
+    int8_t* padded = reinterpret_cast<int8_t*>(scratch);
+    if (bl::launch_pad_codes(xq, M, K, padded_codes(K), padded, st) != cudaSuccess) return BL_ERR_CUDA;
+    xq = padded;
+    scratch += round256(static_cast<size_t>(M * padded_codes(K)));
+  }
+  if (fmt != BL_PACK_I2) {
+    const cudaError_t e = fmt == BL_PACK_T5 ? bl::launch_t5_to_i2(packed, N, K, rb, scratch, rb2, st)
+                                            : bl::launch_b1_to_i2(packed, N, K, rb, scratch, rb2, st);
+    if (e != cudaSuccess) return BL_ERR_CUDA;
+    packed = scratch;
+    scratch += round256(static_cast<size_t>(N * rb2));
+  }
+  int8_t* w8 = reinterpret_cast<int8_t*>(scratch);
+  if (bl::launch_i2_to_i8(packed, N, rb2, w8, st) != cudaSuccess) return BL_ERR_CUDA;
+  return cuda_status(bl::launch_gemm_i8(xq, padded_codes(K), w8, 4 * rb2, gamma, scale, y, ydt, M, N, K, ep, ws, st));
 }
 
 // Several weight matrices sharing one token batch (for example a block's Q, K

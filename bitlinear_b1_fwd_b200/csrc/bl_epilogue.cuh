@@ -139,36 +139,4 @@ __device__ __forceinline__ void epilogue_act(int act, uint32_t (&acc)[NC]) {
   }
 }
 
-// NC outputs of one column n held as INT32 sums by a tensor-core epilogue
-// thread, for consecutive tokens: acc[j] becomes the bits of the fp32 output.
-// cf[j]: the tokens' dequantization factors; bias: the column's; o: the first
-// token's element of y, tokens ld elements apart; live: tokens to read (0 when
-// the column is past N).  keep(j, z) receives the pre-activations when they
-// are kept.
-template <int NC, typename Keep>
-__device__ __forceinline__ void epilogue_chunk(const Epilogue& ep, uint32_t (&acc)[NC], const float* cf, float bias,
-                                               int ydt, int64_t o, int64_t ld, int live, Keep keep) {
-#pragma unroll
-  for (int j = 0; j < NC; ++j)
-    acc[j] = __float_as_uint(__fmul_rn(__int2float_rn(static_cast<int>(acc[j])), cf[j]));
-  if (ep.act < 0) return;
-#pragma unroll
-  for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(__fadd_rn(__uint_as_float(acc[j]), bias));
-  if (ep.pre != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NC; ++j) keep(j, __uint_as_float(acc[j]));
-  }
-  if (ydt == BL_BF16)
-    epilogue_act<NC, true>(ep.act, acc);
-  else
-    epilogue_act<NC, false>(ep.act, acc);
-  if (ep.res != nullptr) {
-    float r[NC];  // all loads in flight together
-#pragma unroll
-    for (int j = 0; j < NC; ++j) r[j] = j < live ? load_out(ep.res, ydt, o + j * ld) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) acc[j] = __float_as_uint(__fadd_rn(__uint_as_float(acc[j]), r[j]));
-  }
-}
-
 }  // namespace bl

@@ -245,7 +245,7 @@ cudaError_t launch_few_fmt(const uint8_t* packed, int64_t rb, const float* gamma
 // Tokens and sizes for which reading all codes in every block of 16 rows (M K N
 // / 16 bytes through L2) costs less than the tensor-memory path's extra passes.
 bool gemm_few_fits(int64_t M, int64_t N, int64_t K) {
-  return M > kGemvMaxTokens && M <= 64 && M * K * ((N + kFewRows - 1) / kFewRows) <= kFewCodeBytes;
+  return M > kEpilogueGemvTokens && M <= 64 && M * K * ((N + kFewRows - 1) / kFewRows) <= kFewCodeBytes;
 }
 
 size_t gemm_few_bytes(int64_t M, int64_t rowbytes, int fmt) {

@@ -74,15 +74,26 @@ __device__ __forceinline__ uint64_t k_major_desc(uint32_t saddr) {
 constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(256 >> 3) << 17) |
                             (static_cast<uint32_t>(256 >> 4) << 24);
 
+template <int YDT>
+struct OutElem;
+template <>
+struct OutElem<BL_F32> {
+  using type = uint32_t;
+};
+template <>
+struct OutElem<BL_BF16> {
+  using type = uint16_t;
+};
+
 // YDT: the type of y, residual and kept pre-activation
 template <int YDT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
-                   const __grid_constant__ CUtensorMap tm_p, const float* __restrict__ gamma,
-                   const float* __restrict__ scale, int M, int N, int K, WsHeader* __restrict__ hdr, long long limit,
-                   const Epilogue ep_arg) {
-  pdl_enter(gamma, scale, hdr);
+                   const __grid_constant__ CUtensorMap tm_p, int o_tma, const float* __restrict__ gamma,
+                   const float* __restrict__ scale, void* __restrict__ y, int M, int N, int K,
+                   WsHeader* __restrict__ hdr, long long limit, const Epilogue ep_arg) {
+  pdl_enter(gamma, scale, y, hdr);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;                   // kStages x [x plane, W plane], swizzled
@@ -205,6 +216,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* box = boxes + 2 * e * kBox;
     uint8_t* row = box + lane * 64;  // this lane's token, its 16-byte pieces in the 64-byte swizzle
     auto piece = [&](int c) { return reinterpret_cast<uint4*>(row + ((c ^ ((lane >> 1) & 3)) << 4)); };
+    // Rows of y that are no multiple of 16 bytes have no tensor map: the warp
+    // copies between its box and an array itself, neighbouring lanes neighbouring
+    // columns (tokens i0 .., columns c .. of the array).
+    using Elem = typename OutElem<YDT>::type;
+    auto cell = [&](uint8_t* bx, int r, int c) {  // token r, column c of a box
+      const int at = c * static_cast<int>(sizeof(Elem));
+      return reinterpret_cast<Elem*>(bx + r * 64 + ((((at >> 4) ^ ((r >> 1) & 3)) << 4) | (at & 15)));
+    };
+    auto box_in = [&](uint8_t* bx, const void* src, int i0, int c0) {
+#pragma unroll 4
+      for (int r = lane / NC; r < 32; r += 32 / NC) {
+        const int c = lane % NC;
+        if (i0 + r < M && c0 + c < N)
+          *cell(bx, r, c) = __ldcg(static_cast<const Elem*>(src) + static_cast<int64_t>(i0 + r) * N + c0 + c);
+      }
+    };
+    auto box_out = [&](void* dst, uint8_t* bx, int i0, int c0) {
+#pragma unroll 4
+      for (int r = lane / NC; r < 32; r += 32 / NC) {
+        const int c = lane % NC;
+        if (i0 + r < M && c0 + c < N)
+          static_cast<Elem*>(dst)[static_cast<int64_t>(i0 + r) * N + c0 + c] = *cell(bx, r, c);
+      }
+    };
     uint32_t res_phase = 0;
     int tc = 0;
     bool ok = true;
@@ -236,9 +271,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool live = ok && i0 < M && j0 + c0 < N;  // (uniform)
         if (lane == 0) bulk_wait_read<0>();  // the stores issued from the boxes have read them
         __syncwarp();
-        if (live && ep.res != nullptr && lane == 0) {
-          mbar_expect_tx(resf + e, kBox);
-          tma_load_2d(box, &tm_r, resf + e, j0 + c0, i0);
+        if (live && ep.res != nullptr) {
+          if (!o_tma) {
+            box_in(box, ep.res, i0, j0 + c0);
+          } else if (lane == 0) {
+            mbar_expect_tx(resf + e, kBox);
+            tma_load_2d(box, &tm_r, resf + e, j0 + c0, i0);
+          }
         }
         uint32_t v[NC];
         if (ok) {
@@ -282,7 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ep.pre != nullptr) put(kBox);
         epilogue_act<NC, YDT == BL_BF16>(ep.act, v);
         if (ep.res != nullptr) {
-          if (!wait_warp(resf + e, res_phase, limit, abort_flag)) {
+          if (!o_tma) {
+            __syncwarp();
+          } else if (!wait_warp(resf + e, res_phase, limit, abort_flag)) {
             if (lane == 0) {
               fail(0x532);
               (void)wait_drain(resf + e, res_phase, limit);
@@ -308,6 +349,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         put(0);
+        if (!o_tma) {
+          __syncwarp();
+          box_out(y, box, i0, j0 + c0);
+          if (ep.pre != nullptr) box_out(ep.pre, box + kBox, i0, j0 + c0);
+          continue;
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -348,12 +395,6 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-// Rows of y that are multiples of 16 bytes (TMA), and tokens enough to pay for
-// writing the int8 weights.
-bool gemm_i8_fits(int64_t M, int64_t N, int ydt) {
-  return M >= kGemmI8Tokens && N * (ydt == BL_F32 ? 4 : 2) % 16 == 0;
-}
-
 cudaError_t launch_i2_to_i8(const uint8_t* i2, int64_t N, int64_t rowbytes, int8_t* w, cudaStream_t st) {
   const int64_t words = N * (rowbytes / 4), cap = static_cast<int64_t>(device_sms()) * 8, g = (words + 255) / 256;
   return launch_pdl(i2_to_i8_kernel, static_cast<unsigned>(g < cap ? g : cap), 256, 0, st,
@@ -372,16 +413,18 @@ cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64
   auto box_map = [&](CUtensorMap* m, const void* p) {
     return encode_out_2d(m, const_cast<void*>(p), ydt == BL_F32, static_cast<uint64_t>(N), static_cast<uint64_t>(M));
   };
-  if (!box_map(&ty, y)) return cudaErrorInvalidValue;
+  const int o_tma = N * (ydt == BL_F32 ? 4 : 2) % 16 == 0 ? 1 : 0;
+  memset(&ty, 0, sizeof ty);
+  if (o_tma && !box_map(&ty, y)) return cudaErrorInvalidValue;
   tr = tp = ty;
-  if (ep.res != nullptr && !box_map(&tr, ep.res)) return cudaErrorInvalidValue;
-  if (ep.pre != nullptr && !box_map(&tp, ep.pre)) return cudaErrorInvalidValue;
+  if (o_tma && ep.res != nullptr && !box_map(&tr, ep.res)) return cudaErrorInvalidValue;
+  if (o_tma && ep.pre != nullptr && !box_map(&tp, ep.pre)) return cudaErrorInvalidValue;
   auto kern = ydt == BL_F32 ? gemm_i8_kernel<BL_F32> : gemm_i8_kernel<BL_BF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((N + 2 * kTile - 1) / (2 * kTile)) * ((M + 2 * kTile - 1) / (2 * kTile));
   const int64_t most = device_sms() / 2, pairs = tiles < most ? tiles : most;
-  e = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kThreads, kSmem, st, tx, tw, ty, tr, tp, gamma, scale,
+  e = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kThreads, kSmem, st, tx, tw, ty, tr, tp, o_tma, gamma, scale, y,
                  static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), static_cast<WsHeader*>(ws), kTimeout,
                  ep);
   return e != cudaSuccess ? e : cudaGetLastError();

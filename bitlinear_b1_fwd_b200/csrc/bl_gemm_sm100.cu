@@ -28,7 +28,6 @@
 #include <cstring>
 
 #include "bl_common.cuh"
-#include "bl_epilogue.cuh"
 #include "bl_kernels.h"
 #include "bl_sm100.cuh"
 #include "bl_tensormap.h"
@@ -36,6 +35,7 @@
 namespace bl {
 namespace {
 
+constexpr int kGemmThreads = 384;  // warp 0 TMA, 1 MMA, 4-7 expansion, 8-11 epilogue
 constexpr int kBN = 128;  // weight rows per tile = MMA M
 constexpr int kBK = 128;  // K per stage = 4 MMAs of K = 32
 constexpr uint32_t kPackedStage = kBN * kBK / 4;  // 4096 bytes
@@ -160,8 +160,7 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
     gemm_i2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, int y_tma, const float* __restrict__ gamma,
                    const float* __restrict__ scale, void* __restrict__ y, int ydt, int M, int N, int K, int ldy, int ks,
-                   int32_t* __restrict__ part, WsHeader* __restrict__ hdr, long long limit, int skip_producer,
-                   const Epilogue ep_arg) {
+                   int32_t* __restrict__ part, WsHeader* __restrict__ hdr, long long limit, int skip_producer) {
   pdl_enter(gamma, scale, y, part, hdr);
   using Cfg = GemmCfg<BT>;
   constexpr int SX = Cfg::kSX, SP = Cfg::kSP, SB = Cfg::kSB;
@@ -372,13 +371,11 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
     const uint32_t esz = (ydt == BL_BF16) ? 2u : 4u;
     const bool use_tma = y_tma != 0 && ks == 1;
     const float g = __ldcg(gamma);
-    const Epilogue ep = epilogue_after_wait(ep_arg);
     int tc = 0, chunk = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++tc) {
       const Unit w = unit_of(u);
       const int a = tc & 1;
       const int n = w.n_t * kBN + 32 * q + lane;
-      const float bias = (ep.bias != nullptr && n < N) ? __ldcg(ep.bias + n) : 0.0f;
       // dequant factor c_t = (gamma s_t) / 127 of each token of the tile, once
       float* cf = cfac + a * BT;
       if (ks == 1)
@@ -408,12 +405,6 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
         tmem_load<Cfg::kChunk>(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * BT + j0),
                                acc);
         const int t0 = w.t_t * BT + j0;
-        if (ks == 1 && ydt != BL_I32)
-          epilogue_chunk<Cfg::kChunk>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy,
-                                      n < N ? M - t0 : 0, [&](int j, float z) {
-                                        if (n < N && t0 + j < M)
-                                          store_out(ep.pre, ydt, static_cast<int64_t>(t0 + j) * ldy + n, z);
-                                      });
         if (ks > 1) {
           if (n < N) {
 #pragma unroll
@@ -433,7 +424,7 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
             if (ydt == BL_I32) {
               *reinterpret_cast<int32_t*>(col + j * 128 * 4) = v;
             } else {
-              const float yv = __uint_as_float(acc[j]);
+              const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
               if (ydt == BL_F32)
                 *reinterpret_cast<float*>(col + j * 128 * 4) = yv;
               else
@@ -454,7 +445,7 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
               if (ydt == BL_I32) {
                 static_cast<int32_t*>(y)[o] = v;
               } else {
-                const float yv = __uint_as_float(acc[j]);
+                const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
                 if (ydt == BL_F32)
                   static_cast<float*>(y)[o] = yv;
                 else
@@ -485,18 +476,24 @@ __global__ void __launch_bounds__(GemmCfg<BT>::kThreads, 1)
 // Four consecutive outputs per thread when N % 4 == 0.
 __global__ void __launch_bounds__(256)
     splitk_reduce_kernel(const int32_t* __restrict__ part, int ks, int M, int N, int ldy, const float* __restrict__ gamma,
-                         const float* __restrict__ scale, void* __restrict__ y, int ydt, const Epilogue ep_arg) {
+                         const float* __restrict__ scale, void* __restrict__ y, int ydt) {
   pdl_enter(part, gamma, scale, y);
-  const Epilogue ep = epilogue_after_wait(ep_arg);
   __shared__ float sh_g;  // gamma once per CTA
   if (threadIdx.x == 0) sh_g = __ldcg(gamma);
   __syncthreads();
   const float g = sh_g;
   const int64_t plane = static_cast<int64_t>(M) * N;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  auto emit = [&](int t, int64_t n, int v) {  // row stride ldy
-    const float cf = ydt == BL_I32 ? 0.0f : dequant_factor(g, __ldcg(scale + t));
-    epilogue_store(ep, y, ydt, static_cast<int64_t>(t) * ldy + n, n, v, cf);
+  auto emit = [&](int64_t o, int t, int v) {
+    if (ydt == BL_I32) {
+      static_cast<int32_t*>(y)[o] = v;
+    } else {
+      const float yv = __fmul_rn(__int2float_rn(v), dequant_factor(g, __ldcg(scale + t)));
+      if (ydt == BL_F32)
+        static_cast<float*>(y)[o] = yv;
+      else
+        static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(yv);
+    }
   };
   if ((N % 4) == 0) {
     const int64_t n4 = plane / 4;
@@ -511,18 +508,18 @@ __global__ void __launch_bounds__(256)
       }
       const int64_t o = 4 * i;
       const int t = static_cast<int>(o / N);
-      const int64_t n = o - static_cast<int64_t>(t) * N;
-      emit(t, n, s.x);
-      emit(t, n + 1, s.y);
-      emit(t, n + 2, s.z);
-      emit(t, n + 3, s.w);
+      const int64_t yo = static_cast<int64_t>(t) * ldy + (o - static_cast<int64_t>(t) * N);  // row stride ldy
+      emit(yo, t, s.x);
+      emit(yo + 1, t, s.y);
+      emit(yo + 2, t, s.z);
+      emit(yo + 3, t, s.w);
     }
   } else {
     for (int64_t o = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; o < plane; o += stride) {
       int s = __ldcg(part + o);
       for (int kz = 1; kz < ks; ++kz) s += __ldcg(part + kz * plane + o);
       const int t = static_cast<int>(o / N);
-      emit(t, o - static_cast<int64_t>(t) * N, s);
+      emit(static_cast<int64_t>(t) * ldy + (o - static_cast<int64_t>(t) * N), t, s);
     }
   }
 }
@@ -543,7 +540,6 @@ __global__ void __launch_bounds__(256)
 constexpr int kStagesA = 5;  // TMA ring: x half + packed tile per stage
 constexpr int kStagesB = 5;  // expanded-weight ring
 constexpr uint32_t kYStage = 32 * 128 * 4;  // output staging: 32 tokens x 128 rows, up to 4 bytes each
-constexpr int kGemm2Threads = 512;          // warp 0 TMA, 1 MMA, 4-7 expansion, 8-15 epilogue
 
 template <int BT>
 struct Gemm2Cfg {
@@ -574,12 +570,11 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
 }
 
 template <int BT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_i2_2sm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                       const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_p, int y_tma,
-                       const float* __restrict__ gamma,
+                       const __grid_constant__ CUtensorMap tm_y, int y_tma, const float* __restrict__ gamma,
                        const float* __restrict__ scale, void* __restrict__ y, int ydt, int M, int N, int K, int ldy,
-                       WsHeader* __restrict__ hdr, long long limit, const Epilogue ep_arg) {
+                       WsHeader* __restrict__ hdr, long long limit) {
   pdl_enter(gamma, scale, y, hdr);
   using Cfg = Gemm2Cfg<BT>;
   extern __shared__ uint8_t smem_raw[];
@@ -622,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf + a, 1);
-      mbar_init(acce + a, 16);
+      mbar_init(acce + a, 8);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -734,32 +729,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
     }
   } else if (warp >= 8) {
     // ------------------------------ epilogue (both CTAs) ------------------------
-    // Two groups of four warps take the 32-token chunks of the tile's accumulator
-    // in turn.  A chunk is converted into the group's shared staging buffer, laid
-    // out as the output tile [32 tokens x 128 rows], and written by one TMA
-    // tensor store (the TMA unit clips rows past N and tokens past M); a buffer
-    // is rewritten only after the stores issued from it have read it.  A bf16
-    // tile takes half the buffer: two of them alternate, or the other half holds
-    // the kept pre-activations, stored the same way.  Without a tensor map for y
-    // (a row of y not a multiple of 16 bytes) the lanes store directly.
-    const int q = warp & 3, et = threadIdx.x - 256, grp = (warp - 8) >> 2;
-    const bool issuer = (et & 127) == 0;  // issues its group's stores
-    uint8_t* stage = ystage + grp * kYStage;
+    // Each 32-token chunk of the tile's accumulator is converted into a shared
+    // staging buffer laid out as the output tile [32 tokens x 128 rows] and
+    // written by one TMA tensor store (the TMA unit clips rows past N and
+    // tokens past M); two buffers alternate, a buffer being rewritten only after
+    // the store issued from it two chunks before has read it.  Without a tensor
+    // map for y (a row of y not a multiple of 16 bytes) the lanes store directly.
+    const int q = warp & 3, et = threadIdx.x - 256;
     const uint32_t esz = (ydt == BL_BF16) ? 2u : 4u;
     const float g = __ldcg(gamma);
-    const Epilogue ep = epilogue_after_wait(ep_arg);
-    const bool keep_tma = y_tma && ydt == BL_BF16 && ep.act >= 0 && ep.pre != nullptr;
-    const bool two_bufs = ydt == BL_BF16 && !keep_tma;
-    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
     int tc = 0, chunk = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++tc) {
       const int a = tc & 1;
       const int n_t = tile % n_tiles, t_t = tile / n_tiles;
       const int nbase = n_t * 2 * kBN + static_cast<int>(rank) * kBN;
       const int n = nbase + 32 * q + lane;
-      const float bias = (ep.bias != nullptr && n < N) ? __ldcg(ep.bias + n) : 0.0f;
       float* cf = cfac + a * BT;
-      for (int j = et; j < BT; j += 256) {
+      for (int j = et; j < BT; j += 128) {
         const int t = t_t * BT + j;
         cf[j] = (t < M && ydt != BL_I32) ? dequant_factor(g, __ldcg(scale + t)) : 0.0f;
       }
@@ -768,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
       asm volatile(
           "{\n\t.reg .pred pi, po;\n\t"
           "setp.ne.u32 pi, %1, 0;\n\t"
-          "bar.red.and.pred po, 1, 256, pi;\n\t"
+          "bar.red.and.pred po, 1, 128, pi;\n\t"
           "selp.u32 %0, 1, 0, po;\n\t}"
           : "=r"(ok_all)
           : "r"(ok_w)
@@ -779,45 +765,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
       }
       tc_fence_after();
 #pragma unroll 1
-      for (int j0 = 32 * grp; j0 < BT; j0 += 64, ++chunk) {
+      for (int j0 = 0; j0 < BT; j0 += 32, ++chunk) {
         uint32_t acc[32];
         tmem_load<32>(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * BT + j0), acc);
         const int t0 = t_t * BT + j0;
-        uint8_t* sb = stage + (two_bufs ? (chunk & 1) * (kYStage / 2) : 0);
-        if (y_tma) {  // the stores issued from this buffer have read it
-          if (issuer) {
-            if (two_bufs)
-              bulk_wait_read<1>();
-            else
-              bulk_wait_read<0>();
-          }
-          group_sync();
-        }
-        uint8_t* col = sb + (32 * q + lane) * esz;  // this lane's row in the staged tile
-        if (ydt != BL_I32)
-          epilogue_chunk<32>(ep, acc, cf + j0, bias, ydt, static_cast<int64_t>(t0) * ldy + n, ldy, n < N ? M - t0 : 0,
-                             [&](int j, float z) {
-                               if (keep_tma)
-                                 *reinterpret_cast<__nv_bfloat16*>(col + kYStage / 2 + j * 128 * 2) = __float2bfloat16_rn(z);
-                               else if (n < N && t0 + j < M)
-                                 store_out(ep.pre, ydt, static_cast<int64_t>(t0 + j) * ldy + n, z);
-                             });
         if (y_tma) {
-          if (ydt == BL_BF16) {
+          uint8_t* sb = ystage + (chunk & 1) * kYStage;
+          if (chunk >= 2) {  // the store issued from this buffer two chunks ago has read it
+            if (et == 0) bulk_wait_read<1>();
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+          }
+          uint8_t* col = sb + (32 * q + lane) * esz;  // this lane's row in the staged tile
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              *reinterpret_cast<__nv_bfloat16*>(col + j * 128 * 2) = __float2bfloat16_rn(__uint_as_float(acc[j]));
-          } else {  // fp32 bits or INT32 sums
-#pragma unroll
-            for (int j = 0; j < 32; ++j) *reinterpret_cast<uint32_t*>(col + j * 128 * 4) = acc[j];
+          for (int j = 0; j < 32; ++j) {
+            const int v = static_cast<int>(acc[j]);
+            if (ydt == BL_I32) {
+              *reinterpret_cast<int32_t*>(col + j * 128 * 4) = v;
+            } else {
+              const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
+              if (ydt == BL_F32)
+                *reinterpret_cast<float*>(col + j * 128 * 4) = yv;
+              else
+                *reinterpret_cast<__nv_bfloat16*>(col + j * 128 * 2) = __float2bfloat16_rn(yv);
+            }
           }
           fence_proxy_async_smem();
-          group_sync();
-          if (issuer && nbase < N && t0 < M) {
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (et == 0 && nbase < N && t0 < M) {
             tma_store_2d(&tm_y, sb, nbase, t0);
-            if (keep_tma) tma_store_2d(&tm_p, sb + kYStage / 2, nbase, t0);
           }
-          if (issuer) bulk_commit();
+          if (et == 0) bulk_commit();
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -828,7 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
               if (ydt == BL_I32) {
                 static_cast<int32_t*>(y)[o] = v;
               } else {
-                const float yv = __uint_as_float(acc[j]);
+                const float yv = __fmul_rn(__int2float_rn(v), cf[j0 + j]);
                 if (ydt == BL_F32)
                   static_cast<float*>(y)[o] = yv;
                 else
@@ -842,7 +819,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemm2Threads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + a), 0));
     }
-    if (y_tma && issuer) bulk_wait<0>();  // every output store has landed before the CTA leaves
+    if (y_tma && et == 0) bulk_wait<0>();  // every output store has landed before the CTA leaves
   }
 
   __syncthreads();
@@ -954,9 +931,9 @@ bool encode_y(CUtensorMap* m, void* y, int ydt, int64_t M, int64_t N, int64_t ld
 template <int BT>
 cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int ks, int32_t* part, void* ws,
-                           long long limit, int skip_producer, cudaStream_t st, const Epilogue& ep, int64_t ldx) {
+                           long long limit, int skip_producer, cudaStream_t st) {
   CUtensorMap tx, tw;
-  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(ldx), 128, BT,
+  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K), 128, BT,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!encode_2d_u8(&tw, w, static_cast<uint64_t>(rb), static_cast<uint64_t>(N), static_cast<uint64_t>(rb),
@@ -974,14 +951,14 @@ cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   e = launch_pdl(kern, grid, GemmCfg<BT>::kThreads, smem, st, tx, tw, ty, y_tma, gamma, scale, y, ydt, static_cast<int>(M),
                  static_cast<int>(N), static_cast<int>(K), static_cast<int>(ldy), ks, part, static_cast<WsHeader*>(ws), limit,
-                 skip_producer, ep);
+                 skip_producer);
   if (e != cudaSuccess) return e;
   if (ks > 1) {
     const int64_t work = (N % 4 == 0) ? M * N / 4 : M * N;
     int64_t rgrid = (work + 255) / 256;
     if (rgrid > 8 * sms) rgrid = 8 * sms;
     e = launch_pdl(splitk_reduce_kernel, static_cast<unsigned>(rgrid), 256, 0, st, static_cast<const int32_t*>(part),
-                   ks, static_cast<int>(M), static_cast<int>(N), static_cast<int>(ldy), gamma, scale, y, ydt, ep);
+                   ks, static_cast<int>(M), static_cast<int>(N), static_cast<int>(ldy), gamma, scale, y, ydt);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
@@ -990,9 +967,9 @@ cudaError_t launch_gemm_bt(const int8_t* xq, const uint8_t* w, int64_t rb, const
 template <int BT>
 cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                             void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, void* ws, long long limit,
-                            cudaStream_t st, const Epilogue& ep, int64_t ldx) {
+                            cudaStream_t st) {
   CUtensorMap tx, tw;
-  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(ldx), 128,
+  if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K), 128,
                     BT / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!encode_2d_u8(&tw, w, static_cast<uint64_t>(rb), static_cast<uint64_t>(N), static_cast<uint64_t>(rb),
@@ -1001,8 +978,6 @@ cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, cons
   CUtensorMap ty;
   const int y_tma = encode_y(&ty, y, ydt, M, N, ldy, 32) ? 1 : 0;
   if (!y_tma) memset(&ty, 0, sizeof(ty));
-  CUtensorMap tp = ty;  // the kept pre-activations: laid out like y
-  if (y_tma && ep.act >= 0 && ep.pre != nullptr && !encode_y(&tp, ep.pre, ydt, M, N, ldy, 32)) return cudaErrorInvalidValue;
   auto kern = gemm_i2_2sm_kernel<BT>;
   const size_t smem = Gemm2Cfg<BT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1010,11 +985,11 @@ cudaError_t launch_gemm_2sm(const int8_t* xq, const uint8_t* w, int64_t rb, cons
   const int64_t tiles = ((N + 2 * kBN - 1) / (2 * kBN)) * ((M + BT - 1) / BT);
   const int64_t pairs_max = device_sms() / 2;
   const int64_t pairs = tiles < pairs_max ? tiles : pairs_max;
-  { const cudaError_t le_ = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGemm2Threads, smem, st, tx, tw, ty, tp, y_tma, gamma, scale, y, ydt,
+  { const cudaError_t le_ = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGemmThreads, smem, st, tx, tw, ty, y_tma, gamma, scale, y, ydt,
                                                                      static_cast<int>(M), static_cast<int>(N),
                                                                      static_cast<int>(K), static_cast<int>(ldy),
                                                                      static_cast<WsHeader*>(ws),
-                                                                     limit, ep); if (le_ != cudaSuccess) return le_; }
+                                                                     limit); if (le_ != cudaSuccess) return le_; }
   return cudaGetLastError();
 }
 
@@ -1052,17 +1027,16 @@ int gemm_split_k(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int32_t* part, void* ws,
-                           long long limit_cycles, int skip_producer, cudaStream_t st, const Epilogue& ep, int64_t ldx) {
+                           long long limit_cycles, int skip_producer, cudaStream_t st) {
   const long long limit = limit_cycles > 0 ? limit_cycles : kTimeoutCycles;
-  if (ldx == 0) ldx = K;
   if (M > 128 && !skip_producer)
-    return launch_gemm_2sm<256>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ws, limit, st, ep, ldx);
+    return launch_gemm_2sm<256>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ws, limit, st);
   const int ks = (part != nullptr && !skip_producer) ? gemm_split_k(M, N, K) : 1;
   switch (gemm_token_tile(M)) {
-    case 16: return launch_gemm_bt<16>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
-    case 32: return launch_gemm_bt<32>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
-    case 64: return launch_gemm_bt<64>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
-    default: return launch_gemm_bt<128>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st, ep, ldx);
+    case 16: return launch_gemm_bt<16>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
+    case 32: return launch_gemm_bt<32>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
+    case 64: return launch_gemm_bt<64>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
+    default: return launch_gemm_bt<128>(xq, w, rb, gamma, scale, y, ydt, M, N, K, ldy, ks, part, ws, limit, skip_producer, st);
   }
 }
 
