@@ -238,31 +238,58 @@ bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, 
   return cuda_status(bl::launch_gemm_i2(xq, w2, rb2, gamma, scale, y, ydt, M, N, K, N, part, ws, 0, 0, st));
 }
 
-// The product with its epilogue: the decode kernels for one token, a kernel on
-// packed weights for a few, the product of int8 weights for more.
+// The product with its epilogue has three forms: the decode kernels, the product
+// on packed weights (gemm_few) and the product on int8 weights (gemm_i8).
+//  - One token: the one-token decode kernel of the format where it takes the
+//    shape (3200 -> 8640: 5.6 us against 10.3), else gemm_few (512 -> 512 in base
+//    3: the general decode kernel takes 22.6 us, gemm_few 6.4).
+//  - 2 to 4 tokens of 2-bit weights: the decode kernel's time grows with tokens,
+//    gemm_few's with the weights (2 tokens: 9.0 us against 10.3 for 3200 -> 8640,
+//    7.8 against 6.6 for 3200 -> 3200; 3 tokens: 26.6 against 36.9 for 8192 ->
+//    28672, 14.1 against 11.5 for 8640 -> 3200).
+//  - Up to 64 tokens, MB of them in groups of 8, 16, 32 or 64: gemm_few takes some
+//    3 us + (2 + MB / 20 + 0.6 K / 1000) us for each turn of its blocks of 16 rows
+//    on the SMs (two fit up to MB = 16), gemm_i8 some 11 us (8 more for odd rows)
+//    + 2.6 NK / 10^7 us (writing and reading the int8 weights) + 0.27 us a k-block
+//    of the busiest SM pair (16 tokens, 3200 -> 8640: 15.4 us against 24.4; 64
+//    tokens: 31.1 against 23.0; 64 tokens, 8192 -> 8192: 36.4 against 43.6).
 enum class ForwardPath { kGemv, kFew, kMany };
-static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K) {
-  return M <= bl::kEpilogueGemvTokens ? ForwardPath::kGemv
-         : bl::gemm_few_fits(M, N, K) ? ForwardPath::kFew
-                                      : ForwardPath::kMany;
+static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
+  const int64_t rb = bitlinear_packed_row_bytes(K, fmt);
+  const double nk = static_cast<double>(N) * static_cast<double>(K) * 1e-7;
+  if (M == 1) {
+    const bool fits = fmt == BL_PACK_I2   ? bl::gemv1_fits(N, K, rb, xdt)
+                      : fmt == BL_PACK_T5 ? bl::gemv1_t5_fits(N, K, rb, xdt)
+                                          : bl::gemv1_b1_fits(N, K, rb, xdt);
+    return fits ? ForwardPath::kGemv : ForwardPath::kFew;
+  }
+  if (M <= bl::kGemvMaxTokens && fmt == BL_PACK_I2 && bl::gemv_max_tokens(fmt, rb) >= 1 &&
+      nk * 1e7 >= static_cast<double>(int64_t{1} << (20 + 2 * M)))
+    return ForwardPath::kGemv;
+  if (M > bl::kFewTokens) return ForwardPath::kMany;
+  const int64_t tiles = (N + 255) / 256, ks = bl::gemm_i8_parts(M, N, K), pairs = bl::device_sms() / 2;
+  const double mb = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int64_t fit = bl::device_sms() * (mb <= 16 ? 2 : 1), turns = ((N + 15) / 16 + fit - 1) / fit;
+  const double few = 3 + static_cast<double>(turns) * (2 + mb / 20 + 0.0006 * static_cast<double>(K));
+  const double many = 11 + (N % 8 != 0 || K % 16 != 0 ? 8 : 0) + 2.6 * nk +
+                      0.27 * static_cast<double>((tiles * ks + pairs - 1) / pairs * ((K + 127) / 128 / ks));
+  return few <= many ? ForwardPath::kFew : ForwardPath::kMany;
 }
 static int64_t padded_codes(int64_t K) { return (K + 15) / 16 * 16; }  // TMA rows
 
 size_t bitlinear_forward_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
   if (!m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
-  const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
   size_t bytes = BL_WS_HEADER_BYTES;
-  switch (epilogue_path(M, N, K)) {
-    case ForwardPath::kGemv:
-      if (b1_via_i2(fmt, K)) bytes += round256(static_cast<size_t>(N * rb2));
-      return bytes;
+  if (M == 0 || N == 0) return bytes;
+  switch (epilogue_path(M, N, K, fmt, xdt)) {
+    case ForwardPath::kGemv: return bytes;
     case ForwardPath::kFew: return bytes + bl::gemm_few_bytes(M, bitlinear_packed_row_bytes(K, fmt), fmt);
     default: break;
   }
-  if (xdt != BL_I8) bytes += round256(static_cast<size_t>(M * K));
-  if (K % 16 != 0) bytes += round256(static_cast<size_t>(M * padded_codes(K)));
-  if (fmt != BL_PACK_I2) bytes += round256(static_cast<size_t>(N * rb2));
-  return bytes + round256(static_cast<size_t>(N * 4 * rb2));
+  if (xdt != BL_I8 || K % 16 != 0) bytes += round256(static_cast<size_t>(M * padded_codes(K)));
+  bytes += round256(static_cast<size_t>(N * bl::gemm_i8_row(K, fmt)));
+  const int ks = bl::gemm_i8_parts(M, N, K);
+  return ks > 1 ? bytes + round256(static_cast<size_t>(ks) * M * N * sizeof(int32_t)) : bytes;
 }
 
 bl_status bitlinear_forward_epilogue(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
@@ -282,43 +309,25 @@ bl_status bitlinear_forward_epilogue(const uint8_t* packed, int fmt, const float
   if (ws_bytes < bitlinear_forward_epilogue_workspace_bytes(M, N, K, fmt, xdt)) return BL_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* scratch = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
-  const int64_t rb = bitlinear_packed_row_bytes(K, fmt), rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
+  const int64_t rb = bitlinear_packed_row_bytes(K, fmt);
   const bl::Epilogue ep{bias, residual, preact, act};
-  const ForwardPath path = epilogue_path(M, N, K);
+  const ForwardPath path = epilogue_path(M, N, K, fmt, xdt);
   if (path == ForwardPath::kFew)
     return cuda_status(bl::launch_gemm_few(packed, fmt, rb, gamma, N, K, x, xdt, scale, M, y, ydt, ep, scratch, st));
-  if (path == ForwardPath::kGemv) {
-    if (b1_via_i2(fmt, K)) {
-      if (bl::launch_b1_to_i2(packed, N, K, rb, scratch, rb2, st) != cudaSuccess) return BL_ERR_CUDA;
-      packed = scratch;
-      fmt = BL_PACK_I2;
-    }
-    if (bl::gemv_max_tokens(fmt, bitlinear_packed_row_bytes(K, fmt)) < 1) return BL_ERR_UNSUPPORTED;
+  if (path == ForwardPath::kGemv)
     return cuda_status(bl::launch_gemv(packed, fmt, gamma, N, K, x, xdt, scale, M, y, ydt, bl::one_group(N, ep), ws, st));
-  }
   const int8_t* xq = static_cast<const int8_t*>(x);
-  if (xdt != BL_I8) {
-    int8_t* codes = reinterpret_cast<int8_t*>(scratch);
-    if (bl::launch_act_quant(x, xdt, M, K, codes, scale, st) != cudaSuccess) return BL_ERR_CUDA;
-    xq = codes;
-    scratch += round256(static_cast<size_t>(M * K));
-  }
-  if (K % 16 != 0) {
-    int8_t* padded = reinterpret_cast<int8_t*>(scratch);
-    if (bl::launch_pad_codes(xq, M, K, padded_codes(K), padded, st) != cudaSuccess) return BL_ERR_CUDA;
-    xq = padded;
+  int8_t* codes = nullptr;
+  if (xdt != BL_I8 || K % 16 != 0) {
+    xq = codes = reinterpret_cast<int8_t*>(scratch);
     scratch += round256(static_cast<size_t>(M * padded_codes(K)));
   }
-  if (fmt != BL_PACK_I2) {
-    const cudaError_t e = fmt == BL_PACK_T5 ? bl::launch_t5_to_i2(packed, N, K, rb, scratch, rb2, st)
-                                            : bl::launch_b1_to_i2(packed, N, K, rb, scratch, rb2, st);
-    if (e != cudaSuccess) return BL_ERR_CUDA;
-    packed = scratch;
-    scratch += round256(static_cast<size_t>(N * rb2));
-  }
   int8_t* w8 = reinterpret_cast<int8_t*>(scratch);
-  if (bl::launch_i2_to_i8(packed, N, rb2, w8, st) != cudaSuccess) return BL_ERR_CUDA;
-  return cuda_status(bl::launch_gemm_i8(xq, padded_codes(K), w8, 4 * rb2, gamma, scale, y, ydt, M, N, K, ep, ws, st));
+  scratch += round256(static_cast<size_t>(N * bl::gemm_i8_row(K, fmt)));
+  if (bl::launch_gemm_operands(packed, fmt, rb, N, K, w8, x, xdt, M, padded_codes(K), codes, scale, st) != cudaSuccess)
+    return BL_ERR_CUDA;
+  return cuda_status(bl::launch_gemm_i8(xq, padded_codes(K), w8, bl::gemm_i8_row(K, fmt), gamma, scale, y, ydt, M, N, K,
+                                        ep, reinterpret_cast<int32_t*>(scratch), ws, st));
 }
 
 // Several weight matrices sharing one token batch (for example a block's Q, K

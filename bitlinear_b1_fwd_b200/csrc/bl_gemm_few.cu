@@ -20,7 +20,7 @@
 // there are fewer chunks than warps, the token groups), and their INT32 sums meet
 // in shared memory by integer adds, whose order does not matter.  Each block
 // reads all codes, M K bytes through L2, which is what limits the number of
-// tokens (see few_fits).
+// tokens it serves well.
 #include "bl_common.cuh"
 #include "bl_epilogue.cuh"
 #include "bl_gemv.cuh"
@@ -42,12 +42,6 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint
   asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// 16 bits -> 16 int8 in {-1, 1}: four bits at a time to the low bits of four bytes
-__device__ __forceinline__ uint4 expand16_bits(uint32_t h) {
-  auto four = [](uint32_t b) { return ~(((b & 0xfu) * 0x00204081u & 0x01010101u) * 0xfeu); };
-  return make_uint4(four(h), four(h >> 4), four(h >> 8), four(h >> 12));
 }
 
 // The int8 weights of word w of a segment.  For base 3, seg holds the segment's
@@ -241,12 +235,6 @@ cudaError_t launch_few_fmt(const uint8_t* packed, int64_t rb, const float* gamma
 }
 
 }  // namespace
-
-// Tokens and sizes for which reading all codes in every block of 16 rows (M K N
-// / 16 bytes through L2) costs less than the tensor-memory path's extra passes.
-bool gemm_few_fits(int64_t M, int64_t N, int64_t K) {
-  return M > kEpilogueGemvTokens && M <= 64 && M * K * ((N + kFewRows - 1) / kFewRows) <= kFewCodeBytes;
-}
 
 size_t gemm_few_bytes(int64_t M, int64_t rowbytes, int fmt) {
   return static_cast<size_t>(few_chunks(rowbytes)) * few_words(fmt) * 8 * few_groups(M) * 4 * 16;

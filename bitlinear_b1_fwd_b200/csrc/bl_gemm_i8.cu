@@ -8,8 +8,8 @@
 // again for every 256 tokens, in the warps' issue slots and shared memory that a
 // rich epilogue needs too: 4096 x 3200 -> 8640 with SiLU and the kept
 // pre-activation took 176 us there, 118 us with neither.  Here one pass writes
-// the weights as int8 rows (N K bytes, 7 us for that layer) and the product only
-// moves tiles and computes.
+// the weights as int8 rows (N K bytes) beside the tokens' codes, and the product
+// only moves tiles and computes.
 //
 // A cluster of two CTAs computes 256 tokens x 256 weight rows
 // (tcgen05.mma.cta_group::2, M = tokens): each CTA stages 128 tokens and 128
@@ -27,6 +27,7 @@
 
 #include "bl_common.cuh"
 #include "bl_epilogue.cuh"
+#include "bl_gemv.cuh"
 #include "bl_kernels.h"
 #include "bl_sm100.cuh"
 #include "bl_tensormap.h"
@@ -81,17 +82,22 @@ struct OutElem<BL_F32> {
   using type = uint32_t;
 };
 template <>
+struct OutElem<BL_I32> {
+  using type = uint32_t;
+};
+template <>
 struct OutElem<BL_BF16> {
   using type = uint16_t;
 };
 
-// YDT: the type of y, residual and kept pre-activation
+// YDT: the type of y, residual and kept pre-activation; BL_I32: no epilogue, the
+// INT32 sums of part kz of a cut contraction go to plane kz of y ([ks][M][N]).
 template <int YDT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
                    const __grid_constant__ CUtensorMap tm_p, int o_tma, const float* __restrict__ gamma,
-                   const float* __restrict__ scale, void* __restrict__ y, int M, int N, int K,
+                   const float* __restrict__ scale, void* __restrict__ y, int M, int N, int K, int ks,
                    WsHeader* __restrict__ hdr, long long limit, const Epilogue ep_arg) {
   pdl_enter(gamma, scale, y, hdr);
   extern __shared__ uint8_t smem_raw[];
@@ -113,7 +119,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   const int kblocks = (K + kBK - 1) / kBK;
   const int j_tiles = (N + 2 * kTile - 1) / (2 * kTile);
-  const int tiles = j_tiles * ((M + 2 * kTile - 1) / (2 * kTile));
+  const int tiles = j_tiles * ((M + 2 * kTile - 1) / (2 * kTile)) * ks;  // ks <= kblocks: no part is empty
+  // tile u: weight rows u % j_tiles, then part of the contraction, then tokens
+  auto tokens_of = [&](int u) { return u / j_tiles / ks * 2 * kTile + static_cast<int>(rank) * kTile; };
+  auto part_of = [&](int u) { return u / j_tiles % ks; };
+  auto first_block = [&](int kz) { return static_cast<int>(static_cast<int64_t>(kz) * kblocks / ks); };
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -153,8 +163,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = pair; u < tiles && ok; u += pairs) {
         const int j0 = (u % j_tiles) * 2 * kTile + static_cast<int>(rank) * kTile;
-        const int i0 = (u / j_tiles) * 2 * kTile + static_cast<int>(rank) * kTile;
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int i0 = tokens_of(u), kz = part_of(u), kb1 = first_block(kz + 1);
+        for (int kb = first_block(kz); kb < kb1; ++kb, ++it) {
           const int s = it % kStages;
           if (!wait1(empty + s, ((it / kStages) & 1) ^ 1, limit, abort_flag)) {
             fail(0x231);
@@ -186,7 +196,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_after();
         const uint32_t d = tmem + static_cast<uint32_t>(a * 2 * kTile);
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int kz = part_of(u), kb0 = first_block(kz), kb1 = first_block(kz + 1);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % kStages;
           if (!wait1(full + s, (it / kStages) & 1, limit, abort_flag)) {
             fail(0x332);
@@ -197,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sa = smem_u32(stages + s * kStage);
 #pragma unroll
           for (int k = 0; k < kBK / 32; ++k)
-            mma_i8_256(d, k_major_desc(sa + 32 * k), k_major_desc(sa + kPlane + 32 * k), kIdesc, (kb | k) != 0);
+            mma_i8_256(d, k_major_desc(sa + 32 * k), k_major_desc(sa + kPlane + 32 * k), kIdesc, kb != kb0 || k != 0);
           commit_pair(empty + s, 0x3);
         }
         if (ok) commit_pair(accf + a, 0x3);
@@ -209,10 +220,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------ epilogue (both CTAs) ------------------------
     // warp: 32 tokens (its tensor-memory lane quarter) x 64 weight rows, in
     // chunks of 64 bytes of y
-    constexpr int NC = YDT == BL_F32 ? 16 : 32, kCols = 64;
+    constexpr int NC = YDT == BL_BF16 ? 32 : 16, kCols = 64;
     const int q = warp & 3, e = warp - 4, part = e >> 2, et = threadIdx.x - 128;
     const float g = __ldcg(gamma);
-    const Epilogue ep = epilogue_after_wait(ep_arg);
+    Epilogue ep = epilogue_after_wait(ep_arg);
+    if constexpr (YDT == BL_I32) ep.res = ep.pre = nullptr;
     uint8_t* box = boxes + 2 * e * kBox;
     uint8_t* row = box + lane * 64;  // this lane's token, its 16-byte pieces in the 64-byte swizzle
     auto piece = [&](int c) { return reinterpret_cast<uint4*>(row + ((c ^ ((lane >> 1) & 3)) << 4)); };
@@ -256,9 +268,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           : "memory");
       if (!go) break;
       const int a = tc & 1;
-      const int i0 = (u / j_tiles) * 2 * kTile + static_cast<int>(rank) * kTile + 32 * q;
+      const int i0 = tokens_of(u) + 32 * q;
       const int jt = (u % j_tiles) * 2 * kTile, j0 = jt + part * kCols;
-      const float cf = i0 + lane < M ? dequant_factor(g, __ldcg(scale + i0 + lane)) : 0.0f;
+      const float cf = YDT != BL_I32 && i0 + lane < M ? dequant_factor(g, __ldcg(scale + i0 + lane)) : 0.0f;
       if (et < 256) bias_s[et] = ep.bias != nullptr && jt + et < N ? __ldcg(ep.bias + jt + et) : 0.0f;
       asm volatile("bar.sync 1, 512;" ::: "memory");
       if (!wait_warp(accf + a, (tc >> 1) & 1, limit, abort_flag)) {
@@ -296,20 +308,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + a), 0));
         }
         if (!live) continue;
-        const float4* bs = reinterpret_cast<const float4*>(bias_s + part * kCols + c0);
+        if constexpr (YDT != BL_I32) {
+          const float4* bs = reinterpret_cast<const float4*>(bias_s + part * kCols + c0);
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-          const float4 b = bs[j / 4];
-          const float bb[4] = {b.x, b.y, b.z, b.w};
+          for (int j = 0; j < NC; j += 4) {
+            const float4 b = bs[j / 4];
+            const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v[j + k] = __float_as_uint(__fadd_rn(__fmul_rn(__int2float_rn(static_cast<int>(v[j + k])), cf), bb[k]));
+            for (int k = 0; k < 4; ++k)
+              v[j + k] = __float_as_uint(__fadd_rn(__fmul_rn(__int2float_rn(static_cast<int>(v[j + k])), cf), bb[k]));
+          }
         }
         auto put = [&](uint32_t at) {  // v as 16-byte pieces of this lane's row of a box
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint4 p;
-            if constexpr (YDT == BL_F32) {
+            if constexpr (YDT != BL_BF16) {
               p = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             } else {
               auto two = [&](int j) { return bf16_pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])); };
@@ -319,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         };
         if (ep.pre != nullptr) put(kBox);
-        epilogue_act<NC, YDT == BL_BF16>(ep.act, v);
+        if constexpr (YDT != BL_I32) epilogue_act<NC, YDT == BL_BF16>(ep.act, v);
         if (ep.res != nullptr) {
           if (!o_tma) {
             __syncwarp();
@@ -338,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              if constexpr (YDT == BL_F32) {
+              if constexpr (YDT != BL_BF16) {
                 v[4 * c + k] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * c + k]), __uint_as_float(w[k])));
               } else {
                 uint32_t* d = v + 8 * c + 2 * k;
@@ -351,14 +365,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         put(0);
         if (!o_tma) {
           __syncwarp();
-          box_out(y, box, i0, j0 + c0);
+          box_out(YDT == BL_I32 ? static_cast<int32_t*>(y) + static_cast<int64_t>(part_of(u)) * M * N : y, box, i0,
+                  j0 + c0);
           if (ep.pre != nullptr) box_out(ep.pre, box + kBox, i0, j0 + c0);
           continue;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&tm_y, box, j0 + c0, i0);
+          if constexpr (YDT == BL_I32)
+            tma_store_3d(&tm_y, box, j0 + c0, i0, part_of(u));
+          else
+            tma_store_2d(&tm_y, box, j0 + c0, i0);
           if (ep.pre != nullptr) tma_store_2d(&tm_p, box + kBox, j0 + c0, i0);
           bulk_commit();
         }
@@ -376,57 +394,271 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// 2-bit rows as int8 rows of 4 rowbytes codes (padding decodes to 0): one packed
-// word (16 weights, 16 output bytes) per item, four in flight.
-__global__ void __launch_bounds__(256)
-    i2_to_i8_kernel(const uint32_t* __restrict__ i2, int64_t words, uint4* __restrict__ w) {
-  pdl_enter(i2, w);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  int64_t s = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (; s + 3 * stride < words; s += 4 * stride) {
-    uint32_t v[4];
+// ---- the operands -------------------------------------------------------------------
+// One launch for both (they are independent, and each alone leaves SMs idle at
+// its end): the first blocks expand weights, the others quantize a token each.
+constexpr int kPrepThreads = 128;
+constexpr int kPrepChunk = 16 * kPrepThreads;  // columns a block turns around in shared memory at a time
+
+// 16-weight word w of a segment of any format as int8.
+template <int FMT>
+__device__ __forceinline__ void expand_segments(const uint8_t* packed, int64_t N, int64_t rowbytes, int64_t ldw,
+                                                uint4* w, int64_t item, int64_t stride) {
+  if constexpr (FMT == BL_PACK_I2) {  // a word per item: rows stay aligned with each other (ldw = 4 rowbytes)
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(packed);
+    const int64_t words = N * (rowbytes / 4);
+    for (; item + 3 * stride < words; item += 4 * stride) {
+      uint32_t v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = __ldcg(i2 + s + u * stride);
+      for (int u = 0; u < 4; ++u) v[u] = __ldcg(src + item + u * stride);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) w[s + u * stride] = expand16(v[u]);
+      for (int u = 0; u < 4; ++u) w[item + u * stride] = expand16(v[u]);
+    }
+    for (; item < words; item += stride) w[item] = expand16(__ldcg(src + item));
+  } else {  // a segment per item: 80 or 128 weights, cut at the row's end
+    constexpr int W = FMT == BL_PACK_T5 ? 5 : 8;
+    const uint32_t segs = static_cast<uint32_t>(rowbytes >> 4);
+    const int64_t items = N * segs, row_words = ldw / 16;
+    for (; item < items; item += stride) {
+      const int64_t n = item / segs, sg = item - n * segs;
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(packed) + item);
+      uint4* dst = w + n * row_words;
+      if constexpr (FMT == BL_PACK_T5) {
+        uint32_t c[5];
+        t5_segment(v, c);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (sg * W + i < row_words) dst[sg * W + i] = expand16(c[i]);
+      } else {
+        const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (sg * W + i < row_words) dst[sg * W + i] = expand16_bits((i & 1) ? c[i >> 1] >> 16 : c[i >> 1]);
+      }
+    }
   }
-  for (; s < words; s += stride) w[s] = expand16(__ldcg(i2 + s));
+}
+
+// Codes of token m in rows of ldx bytes (zeros past K) and its scale (XDT = I8:
+// the codes are given and only take the new row length).  A row's first 4096
+// values are read once and kept in registers.
+template <int XDT>
+__device__ __forceinline__ void quantize_token(const void* x, int64_t m, int64_t K, int64_t ldx, int8_t* xq,
+                                               float* scale, uint8_t* turn, BlockSum& sum) {
+  int8_t* out = xq + m * ldx;
+  if constexpr (XDT != BL_I8) {
+    if (K % 8 == 0) {
+      constexpr int kKeep = 4;
+      Raw<XDT, 8> r[kKeep];
+      float amax = 0.0f;
+      auto take = [&](const Raw<XDT, 8>& q) {
+        float v[8];
+        q.get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+      };
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int64_t k = 8 * (static_cast<int64_t>(i) * kPrepThreads + threadIdx.x);
+        if (k < K) r[i].load(x, m * K + k);
+        else r[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) take(r[i]);
+      for (int64_t k = 8 * (static_cast<int64_t>(kKeep) * kPrepThreads + threadIdx.x); k < K; k += 8 * kPrepThreads) {
+        Raw<XDT, 8> q;
+        q.load(x, m * K + k);
+        take(q);
+      }
+      const float s = fmaxf(sum.max(amax), 1e-6f), c127 = __fdiv_rn(127.0f, s);
+      if (threadIdx.x == 0) scale[m] = s;
+      auto give = [&](const Raw<XDT, 8>& q, int64_t k) {
+        float v[8];
+        int c[8];
+        q.get(v);
+        quant_act_fast_n<8>(v, s, c127, c);
+        *reinterpret_cast<uint2*>(out + k) = make_uint2(pack4(c), pack4(c + 4));
+      };
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int64_t k = 8 * (static_cast<int64_t>(i) * kPrepThreads + threadIdx.x);
+        if (k < K) give(r[i], k);
+      }
+      for (int64_t k = 8 * (static_cast<int64_t>(kKeep) * kPrepThreads + threadIdx.x); k < K; k += 8 * kPrepThreads) {
+        Raw<XDT, 8> q;
+        q.load(x, m * K + k);
+        give(q, k);
+      }
+      if (threadIdx.x == 0 && K < ldx) *reinterpret_cast<uint2*>(out + K) = make_uint2(0u, 0u);
+      return;
+    }
+  }
+  // rows that start anywhere: neighbouring threads load neighbouring values, and
+  // the codes turn around in shared memory into 16-byte stores
+  float s = 1.0f, c127 = 0.0f;
+  if constexpr (XDT != BL_I8) {
+    float amax = 0.0f;
+#pragma unroll 8
+    for (int64_t k = threadIdx.x; k < K; k += kPrepThreads) amax = fmaxf(amax, fabsf(load_elem<XDT>(x, m * K + k)));
+    s = fmaxf(sum.max(amax), 1e-6f);
+    c127 = __fdiv_rn(127.0f, s);
+    if (threadIdx.x == 0) scale[m] = s;
+  }
+  for (int64_t k0 = 0; k0 < ldx; k0 += kPrepChunk) {
+#pragma unroll 8
+    for (int i = 0; i < kPrepChunk / kPrepThreads; ++i) {
+      const int at = i * kPrepThreads + threadIdx.x;
+      const int64_t k = k0 + at;
+      int c = 0;
+      if (k < K) {
+        if constexpr (XDT == BL_I8)
+          c = __ldcg(static_cast<const signed char*>(x) + m * K + k);
+        else
+          c = quant_act_fast(load_elem<XDT>(x, m * K + k), s, c127);
+      }
+      turn[at] = static_cast<uint8_t>(c);
+    }
+    __syncthreads();
+    const int64_t k = k0 + 16 * threadIdx.x;
+    if (k < ldx) *reinterpret_cast<uint4*>(out + k) = *reinterpret_cast<const uint4*>(turn + 16 * threadIdx.x);
+    __syncthreads();
+  }
+}
+
+template <int FMT, int XDT>
+__global__ void __launch_bounds__(kPrepThreads)
+    gemm_operands_kernel(const uint8_t* __restrict__ packed, int64_t N, int64_t K, int64_t rowbytes, int64_t ldw,
+                         uint4* __restrict__ w, int wblocks, const void* __restrict__ x, int64_t M, int64_t ldx,
+                         int8_t* __restrict__ xq, float* __restrict__ scale) {
+  pdl_enter(packed, w, x, xq, scale);
+  if (static_cast<int>(blockIdx.x) < wblocks) {
+    expand_segments<FMT>(packed, N, rowbytes, ldw, w, static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x,
+                         static_cast<int64_t>(wblocks) * kPrepThreads);
+    return;
+  }
+  __shared__ __align__(16) uint8_t turn[kPrepChunk];
+  __shared__ __align__(16) float sum_mem[2][4][32];
+  BlockSum sum(sum_mem);
+  for (int64_t m = blockIdx.x - wblocks; m < M; m += gridDim.x - wblocks)
+    quantize_token<XDT>(x, m, K, ldx, xq, scale, turn, sum);
+}
+
+// The parts of a cut contraction (exact INT32 sums, V = 4 or 1 neighbouring
+// outputs per thread), then the epilogue.
+template <int V>
+__global__ void __launch_bounds__(128)
+    gemm_parts_kernel(const int32_t* __restrict__ part, int ks, int64_t M, int64_t N, const float* __restrict__ gamma,
+                      const float* __restrict__ scale, void* __restrict__ y, int ydt, const Epilogue ep_arg) {
+  pdl_enter(part, gamma, scale, y);
+  const Epilogue ep = epilogue_after_wait(ep_arg);
+  const float g = __ldcg(gamma);
+  const int64_t plane = M * N, stride = static_cast<int64_t>(gridDim.x) * blockDim.x * V;
+  for (int64_t o = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * V; o < plane; o += stride) {
+    int s[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0;
+#pragma unroll 8
+    for (int kz = 0; kz < ks; ++kz) {
+      if constexpr (V == 4) {
+        const int4 p = __ldcg(reinterpret_cast<const int4*>(part + kz * plane + o));
+        s[0] += p.x;
+        s[1] += p.y;
+        s[2] += p.z;
+        s[3] += p.w;
+      } else {
+        s[0] += __ldcg(part + kz * plane + o);
+      }
+    }
+    const int64_t m = o / N, n = o - m * N;
+    const float cf = dequant_factor(g, __ldcg(scale + m));
+#pragma unroll
+    for (int j = 0; j < V; ++j) epilogue_store(ep, y, ydt, o + j, n + j, s[j], cf);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_i2_to_i8(const uint8_t* i2, int64_t N, int64_t rowbytes, int8_t* w, cudaStream_t st) {
-  const int64_t words = N * (rowbytes / 4), cap = static_cast<int64_t>(device_sms()) * 8, g = (words + 255) / 256;
-  return launch_pdl(i2_to_i8_kernel, static_cast<unsigned>(g < cap ? g : cap), 256, 0, st,
-                    reinterpret_cast<const uint32_t*>(i2), words, reinterpret_cast<uint4*>(w));
+// Parts of the contraction: few tiles leave most SMs without work (128 tokens,
+// 8640 -> 3200: 13 tiles, 36 us whole and X us in parts).  The number in 1..16
+// with the least work on the busiest pair of SMs, in k-blocks, plus 3 per tile
+// (filling the ring, the epilogue) and for the pass over the parts 8 and their
+// bytes' worth.
+int gemm_i8_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((N + 2 * kTile - 1) / (2 * kTile)) * ((M + 2 * kTile - 1) / (2 * kTile));
+  const int64_t kblocks = (K + kBK - 1) / kBK, pairs = device_sms() / 2 > 0 ? device_sms() / 2 : 1;
+  int best = 1;
+  int64_t best_cost = -1;
+  for (int ks = 1; ks <= 16 && ks <= kblocks; ++ks) {
+    const int64_t cost = (tiles * ks + pairs - 1) / pairs * ((kblocks + ks - 1) / ks + 3) +
+                         (ks > 1 ? 8 + ks * M * N / 500000 : 0);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = ks;
+    }
+  }
+  return best;
+}
+
+int64_t gemm_i8_row(int64_t K, int fmt) {
+  return fmt == BL_PACK_I2 ? (K + 63) / 64 * 64 : (K + 15) / 16 * 16;
+}
+
+cudaError_t launch_gemm_operands(const uint8_t* packed, int fmt, int64_t rowbytes, int64_t N, int64_t K, int8_t* w,
+                                 const void* x, int xdt, int64_t M, int64_t ldx, int8_t* xq, float* scale,
+                                 cudaStream_t st) {
+  const int64_t items = fmt == BL_PACK_I2 ? N * (rowbytes / 4) / 4 : N * (rowbytes / 16);
+  const int64_t cap = static_cast<int64_t>(device_sms()) * 8, g = (items + kPrepThreads - 1) / kPrepThreads;
+  const int wblocks = static_cast<int>(g < cap ? (g < 1 ? 1 : g) : cap);
+  const int64_t grid = wblocks + (xq == nullptr ? 0 : (M < (1 << 20) ? M : 1 << 20));
+  auto run = [&](auto kern) {
+    return launch_pdl(kern, static_cast<unsigned>(grid), kPrepThreads, 0, st, packed, N, K, rowbytes,
+                      gemm_i8_row(K, fmt), reinterpret_cast<uint4*>(w), wblocks, x, M, ldx, xq, scale);
+  };
+#define BL_GO(FMT)                                                        \
+  return xdt == BL_F32    ? run(gemm_operands_kernel<FMT, BL_F32>)        \
+         : xdt == BL_BF16 ? run(gemm_operands_kernel<FMT, BL_BF16>)       \
+                          : run(gemm_operands_kernel<FMT, BL_I8>)
+  if (fmt == BL_PACK_I2) BL_GO(BL_PACK_I2);
+  if (fmt == BL_PACK_T5) BL_GO(BL_PACK_T5);
+  BL_GO(BL_PACK_B1);
+#undef BL_GO
 }
 
 cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64_t ldw, const float* gamma,
                            const float* scale, void* y, int ydt, int64_t M, int64_t N, int64_t K, const Epilogue& ep,
-                           void* ws, cudaStream_t st) {
+                           int32_t* part, void* ws, cudaStream_t st) {
   CUtensorMap tx, tw, ty, tr, tp;
   if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(ldx), kBK, kTile,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d_u8(&tw, w, static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(ldw), kBK, kTile,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  const int ks = gemm_i8_parts(M, N, K);
+  const int odt = ks > 1 ? static_cast<int>(BL_I32) : ydt;
+  void* out = ks > 1 ? part : y;
   auto box_map = [&](CUtensorMap* m, const void* p) {
-    return encode_out_2d(m, const_cast<void*>(p), ydt == BL_F32, static_cast<uint64_t>(N), static_cast<uint64_t>(M));
+    return encode_out_64(m, const_cast<void*>(p), odt != BL_BF16, static_cast<uint64_t>(N), static_cast<uint64_t>(M),
+                         ks > 1 ? static_cast<uint64_t>(ks) : 0);
   };
-  const int o_tma = N * (ydt == BL_F32 ? 4 : 2) % 16 == 0 ? 1 : 0;
+  const int o_tma = N * (odt == BL_BF16 ? 2 : 4) % 16 == 0 ? 1 : 0;
   memset(&ty, 0, sizeof ty);
-  if (o_tma && !box_map(&ty, y)) return cudaErrorInvalidValue;
+  if (o_tma && !box_map(&ty, out)) return cudaErrorInvalidValue;
   tr = tp = ty;
-  if (o_tma && ep.res != nullptr && !box_map(&tr, ep.res)) return cudaErrorInvalidValue;
-  if (o_tma && ep.pre != nullptr && !box_map(&tp, ep.pre)) return cudaErrorInvalidValue;
-  auto kern = ydt == BL_F32 ? gemm_i8_kernel<BL_F32> : gemm_i8_kernel<BL_BF16>;
+  if (o_tma && ks == 1 && ep.res != nullptr && !box_map(&tr, ep.res)) return cudaErrorInvalidValue;
+  if (o_tma && ks == 1 && ep.pre != nullptr && !box_map(&tp, ep.pre)) return cudaErrorInvalidValue;
+  auto kern = odt == BL_I32 ? gemm_i8_kernel<BL_I32> : odt == BL_F32 ? gemm_i8_kernel<BL_F32> : gemm_i8_kernel<BL_BF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((N + 2 * kTile - 1) / (2 * kTile)) * ((M + 2 * kTile - 1) / (2 * kTile));
+  const int64_t tiles = ((N + 2 * kTile - 1) / (2 * kTile)) * ((M + 2 * kTile - 1) / (2 * kTile)) * ks;
   const int64_t most = device_sms() / 2, pairs = tiles < most ? tiles : most;
-  e = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kThreads, kSmem, st, tx, tw, ty, tr, tp, o_tma, gamma, scale, y,
-                 static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), static_cast<WsHeader*>(ws), kTimeout,
-                 ep);
+  e = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kThreads, kSmem, st, tx, tw, ty, tr, tp, o_tma, gamma, scale,
+                 out, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), ks, static_cast<WsHeader*>(ws),
+                 kTimeout, ep);
+  if (e == cudaSuccess && ks > 1) {
+    const int64_t v = N % 4 == 0 ? 4 : 1, cap = static_cast<int64_t>(device_sms()) * 16, g = (M * N / v + 127) / 128;
+    e = launch_pdl(v == 4 ? gemm_parts_kernel<4> : gemm_parts_kernel<1>, static_cast<unsigned>(g < cap ? g : cap), 128,
+                   0, st, static_cast<const int32_t*>(part), ks, M, N, gamma, scale, y, ydt, ep);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

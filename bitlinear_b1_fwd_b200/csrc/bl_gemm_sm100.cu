@@ -1040,29 +1040,6 @@ cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const
   }
 }
 
-// x_q rows copied to a row stride of ld bytes (a multiple of 16, zeros past K),
-// for TMA: 16 codes per thread.
-__global__ void __launch_bounds__(256)
-    pad_codes_kernel(const uint8_t* __restrict__ src, int64_t M, int64_t K, int64_t ld, uint8_t* __restrict__ dst) {
-  pdl_enter(src, dst);
-  const int64_t per_row = ld / 16, items = M * per_row;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < items; e += stride) {
-    const int64_t m = e / per_row, k = 16 * (e - m * per_row);
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (k + j < K) v[j >> 2] |= static_cast<uint32_t>(__ldcg(src + m * K + k + j)) << (8 * (j & 3));
-    reinterpret_cast<uint4*>(dst)[e] = make_uint4(v[0], v[1], v[2], v[3]);
-  }
-}
-
-cudaError_t launch_pad_codes(const int8_t* src, int64_t M, int64_t K, int64_t ld, int8_t* dst, cudaStream_t st) {
-  const int64_t cap = static_cast<int64_t>(device_sms()) * 8, g = (M * (ld / 16) + 255) / 256;
-  return launch_pdl(pad_codes_kernel, static_cast<unsigned>(g < cap ? g : cap), 256, 0, st,
-                    reinterpret_cast<const uint8_t*>(src), M, K, ld, reinterpret_cast<uint8_t*>(dst));
-}
-
 cudaError_t launch_b1_to_i2(const uint8_t* b1, int64_t N, int64_t K, int64_t rb1, uint8_t* i2, int64_t rb2,
                             cudaStream_t st) {
   const int64_t work = N * (rb2 / 16);

@@ -1306,12 +1306,16 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     }
   }
   __syncthreads();  // every part of every row has been added
-  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = threadIdx.x; r < nrows; r += nthr) {
     const int a = racc[r] - corr;
     const int64_t o = row0 + r;
     const float cf = rg.n == 1 ? cfac : dequant_factor(sh_gam[row_group(rg, o)], s_tok);
-    epilogue_store(ep, y, ydt, o, o, a, cf);
+    if (ydt == BL_I32)
+      static_cast<int32_t*>(y)[o] = a;
+    else if (ydt == BL_F32)
+      static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
+    else
+      static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
   }
 }
 

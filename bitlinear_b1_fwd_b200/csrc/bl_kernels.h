@@ -77,18 +77,21 @@ int gemm_token_tile(int64_t M);
 cudaError_t launch_gemm_i2(const int8_t* xq, const uint8_t* w, int64_t rb, const float* gamma, const float* scale,
                            void* y, int ydt, int64_t M, int64_t N, int64_t K, int64_t ldy, int32_t* part, void* ws,
                            long long limit_cycles, int skip_producer, cudaStream_t st);
-cudaError_t launch_pad_codes(const int8_t* src, int64_t M, int64_t K, int64_t ld, int8_t* dst, cudaStream_t st);
 int gemm_split_k(int64_t M, int64_t N, int64_t K);
 // The product with an epilogue on weights expanded to int8 rows of ldw bytes.
-cudaError_t launch_i2_to_i8(const uint8_t* i2, int64_t N, int64_t rowbytes, int8_t* w, cudaStream_t st);
+// Its operands: weights as int8 rows of gemm_i8_row bytes, codes in rows of ldx
+// bytes (xq null: the codes are there already).
+int64_t gemm_i8_row(int64_t K, int fmt);
+cudaError_t launch_gemm_operands(const uint8_t* packed, int fmt, int64_t rowbytes, int64_t N, int64_t K, int8_t* w,
+                                 const void* x, int xdt, int64_t M, int64_t ldx, int8_t* xq, float* scale,
+                                 cudaStream_t st);
 cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64_t ldw, const float* gamma,
                            const float* scale, void* y, int ydt, int64_t M, int64_t N, int64_t K, const Epilogue& ep,
-                           void* ws, cudaStream_t st);
-// The product with an epilogue of a few tokens, from packed weights; scratch of
-// gemm_few_bytes for the tokens' codes.
-constexpr int64_t kFewCodeBytes = int64_t{48} << 20;
-constexpr int64_t kEpilogueGemvTokens = 4;
-bool gemm_few_fits(int64_t M, int64_t N, int64_t K);
+                           int32_t* part, void* ws, cudaStream_t st);
+int gemm_i8_parts(int64_t M, int64_t N, int64_t K);  // part: [this][M][N], or unused when 1
+// The product with an epilogue of up to 64 tokens, from packed weights; scratch
+// of gemm_few_bytes for the tokens' codes.
+constexpr int64_t kFewTokens = 64;
 size_t gemm_few_bytes(int64_t M, int64_t rowbytes, int fmt);
 cudaError_t launch_gemm_few(const uint8_t* packed, int fmt, int64_t rowbytes, const float* gamma, int64_t N, int64_t K,
                             const void* x, int xdt, float* scale, int64_t M, void* y, int ydt, const Epilogue& ep,

@@ -171,6 +171,12 @@ __device__ __forceinline__ uint4 expand16(uint32_t w) {
   return o;
 }
 
+// 16 bits -> 16 int8 in {-1, 1}: four bits at a time to the low bits of four bytes
+__device__ __forceinline__ uint4 expand16_bits(uint32_t h) {
+  auto four = [](uint32_t b) { return ~(((b & 0xfu) * 0x00204081u & 0x01010101u) * 0xfeu); };
+  return make_uint4(four(h), four(h >> 4), four(h >> 8), four(h >> 12));
+}
+
 // A base-3 segment (16 bytes, 80 weights) as five words of 2-bit codes (a base-3
 // digit is the 2-bit code of the same weight).  With q_i = floor(b / 3^i) the
 // digits of a byte b are d_i = q_i - 3 q_{i+1}, so its ten bits are sum d_i 4^i =
