@@ -637,8 +637,8 @@ cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64
   const int odt = ks > 1 ? static_cast<int>(BL_I32) : ydt;
   void* out = ks > 1 ? part : y;
   auto box_map = [&](CUtensorMap* m, const void* p) {
-    return encode_out_64(m, const_cast<void*>(p), odt != BL_BF16, static_cast<uint64_t>(N), static_cast<uint64_t>(M),
-                         ks > 1 ? static_cast<uint64_t>(ks) : 0);
+    return encode_out(m, const_cast<void*>(p), odt != BL_BF16, static_cast<uint64_t>(N), static_cast<uint64_t>(M),
+                         ks > 1 ? static_cast<uint64_t>(ks) : 0, 64);
   };
   const int o_tma = N * (odt == BL_BF16 ? 2 : 4) % 16 == 0 ? 1 : 0;
   memset(&ty, 0, sizeof ty);

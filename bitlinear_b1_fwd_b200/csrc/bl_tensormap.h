@@ -52,35 +52,22 @@ inline bool encode_2d_b16(CUtensorMap* m, const void* base, uint64_t inner, uint
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [planes x rows x cols] of a 4- or 2-byte float type written by TMA stores from
-// swizzled boxes of 128 bytes x 32 rows.  False when a row is not a multiple of
-// 16 bytes.
-inline bool encode_out_3d(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t planes) {
-  const uint64_t esz = f32 ? 4 : 2;
+// A 4- or 2-byte float array [rows x cols] in boxes of `bytes` (64 or 128, swizzled
+// as such) x 32 rows, for loads (zeros out of bounds) and stores; with planes > 0
+// a third dimension.  False when a row is not a multiple of 16 bytes.
+inline bool encode_out(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t planes,
+                       uint32_t bytes) {
+  const uint32_t esz = f32 ? 4 : 2;
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr || cols * esz % 16 != 0) return false;
   const cuuint64_t dims[3] = {cols, rows, planes};
   const cuuint64_t strides[2] = {cols * esz, rows * cols * esz};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esz), 32, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [rows x cols] in boxes of 64 bytes x 32 rows (64-byte swizzle), for loads
-// (zeros out of bounds) and stores; with planes > 0 a third dimension.
-inline bool encode_out_64(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t planes) {
-  const uint64_t esz = f32 ? 4 : 2;
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr || cols * esz % 16 != 0) return false;
-  const cuuint64_t dims[3] = {cols, rows, planes};
-  const cuuint64_t strides[2] = {cols * esz, rows * cols * esz};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / esz), 32, 1};
+  const cuuint32_t box[3] = {bytes / esz, 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2, base, dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace bl
