@@ -15,6 +15,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbitlinear.so")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 BL_OK, BL_ERR_INVALID_VALUE, BL_ERR_UNSUPPORTED, BL_ERR_MISALIGNED = 0, 1, 2, 3
 BL_ERR_WORKSPACE_TOO_SMALL, BL_ERR_CUDA, BL_ERR_DEVICE_TIMEOUT, BL_ERR_BAD_CODE = 4, 5, 6, 7
@@ -280,73 +281,23 @@ def bitlinear_backward_dw(dy, xq, scale, gamma, dw, stream=None) -> None:
 #
 # These calls check shapes, dtypes, contiguity and that every tensor is on one
 # CUDA device, and run on that device (the current stream there unless one is
-# given); the current device of the caller does not change.
+# given); the current device of the caller does not change.  The checks and the
+# marshalling are compiled (csrc/bl_calls.cpp): in Python they took longer than a
+# launch.
 
-_F32, _BF16, _INT8, _U8 = torch.float32, torch.bfloat16, torch.int8, torch.uint8
-_FLOATS, _ONLY_F32, _ONLY_BF16, _ONLY_I8, _BYTES = (_F32, _BF16), (_F32,), (_BF16,), (_INT8,), (_U8,)
-_INPUTS = (_F32, _BF16, _INT8)
-
-
-def _want(name, t, shape, dtypes, dev):
-    """t is None or a contiguous tensor of this shape and one of the dtypes on dev."""
-    if t is None or (t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous()):
-        return
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    raise ValueError(f"{name} must be contiguous")
+_native = None
 
 
-def _matrix(name, t):
-    """The device of a 2-D CUDA tensor."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-def _workspace(ws, dev):
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {dev}")
-    return ws.data_ptr(), ws.nbytes
-
-
-def _raw(t):
-    return None if t is None else t.data_ptr()
-
-
-# the current stream's handle and the current device without building objects
-# (torch.cuda.current_stream() alone costs 3.2 us, as much as a launch)
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
-def _call(name, dev, stream, *args):
-    """lib().name(*args, stream) on dev."""
-    fn = getattr(_lib or lib(), name)
-    index = dev.index
-    handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == _current_device():
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, handle)
-    if status != BL_OK:
-        raise BitLinearError(status, name)
-
-
-_PER_BYTE = {BL_PACK_I2: 4, BL_PACK_T5: 5, BL_PACK_B1: 8}
-
-
-def _packed_row(K, fmt):
-    """bitlinear_packed_row_bytes(K, fmt)"""
-    per = _PER_BYTE.get(fmt)
-    if per is None or K < 1:
-        return bitlinear_packed_row_bytes(K, fmt)
-    return (-(-K // per) + 15) // 16 * 16
+def _calls():
+    """The compiled marshalling (raises if it, or the library, has not been built)."""
+    global _native
+    if _native is None:
+        lib()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"{CALLS_PATH} is missing: build it first (python -m bitlinear_b1_fwd_b200.build)")
+        from . import _calls as native
+        _native = native
+    return _native
 
 
 def bitlinear_forward_epilogue_workspace_bytes(M: int, N: int, K: int, fmt: int, xdt: int) -> int:
@@ -356,20 +307,10 @@ def bitlinear_forward_epilogue_workspace_bytes(M: int, N: int, K: int, fmt: int,
 def bitlinear_forward_epilogue(packed, fmt, gamma, N, K, x, scale, y, ws, bias=None, act=BL_ACT_NONE, residual=None,
                                preact=None, stream=None) -> None:
     """y = act(x W_q^T dequantized + bias) + residual; preact receives the argument of act."""
-    dev = _matrix("x", x)
-    M = x.shape[0]
-    _want("x", x, (M, K), _INPUTS, dev)
-    _want("packed", packed, (N, _packed_row(K, fmt)), _BYTES, dev)
-    _want("gamma", gamma, (1,), _ONLY_F32, dev)
-    _want("scale", scale, (M,), _ONLY_F32, dev)
-    _want("y", y, (M, N), _FLOATS, dev)
-    _want("bias", bias, (N,), _ONLY_F32, dev)
-    _want("residual", residual, (M, N), (y.dtype,), dev)
-    _want("preact", preact, (M, N), (y.dtype,), dev)
-    wp, wn = _workspace(ws, dev)
-    _call("bitlinear_forward_epilogue", dev, stream, packed.data_ptr(), fmt, gamma.data_ptr(), N, K, x.data_ptr(),
-          _DT[x.dtype], scale.data_ptr(), M, _raw(bias), act, _raw(residual), _raw(preact), y.data_ptr(), _DT[y.dtype],
-          wp, wn)
+    status = (_native or _calls()).forward_epilogue(packed, fmt, gamma, N, K, x, scale, y, ws, bias, act, residual,
+                                                    preact, stream)
+    if status:
+        raise BitLinearError(status, "bitlinear_forward_epilogue")
 
 
 def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
@@ -378,15 +319,9 @@ def bitlinear_epilogue_backward_workspace_bytes(M: int, N: int) -> int:
 
 def bitlinear_epilogue_backward(dy, z, act, dz, dbias, ws, stream=None) -> None:
     """dz = dy act'(z) and dbias = its column sums (either may be None)."""
-    dev = _matrix("dy", dy)
-    M, N = dy.shape
-    _want("dy", dy, (M, N), _FLOATS, dev)
-    _want("z", z, (M, N), _FLOATS, dev)
-    _want("dz", dz, (M, N), (dy.dtype,), dev)
-    _want("dbias", dbias, (N,), _ONLY_F32, dev)
-    wp, wn = _workspace(ws, dev)
-    _call("bitlinear_epilogue_backward", dev, stream, dy.data_ptr(), _DT[dy.dtype], _raw(z),
-          BL_F32 if z is None else _DT[z.dtype], act, M, N, _raw(dz), _raw(dbias), wp, wn)
+    status = (_native or _calls()).epilogue_backward(dy, z, act, dz, dbias, ws, stream)
+    if status:
+        raise BitLinearError(status, "bitlinear_epilogue_backward")
 
 
 def bitlinear_backward_dx_bf16_workspace_bytes(M: int, N: int, K: int, fmt: int) -> int:
@@ -395,15 +330,9 @@ def bitlinear_backward_dx_bf16_workspace_bytes(M: int, N: int, K: int, fmt: int)
 
 def bitlinear_backward_dx_bf16(packed, fmt, gamma, N, K, dz, dx, ws, stream=None) -> None:
     """dx = gamma dz W_q on the tensor cores (bf16 dz, dx bf16 or fp32)."""
-    dev = _matrix("dz", dz)
-    M = dz.shape[0]
-    _want("dz", dz, (M, N), _ONLY_BF16, dev)
-    _want("packed", packed, (N, _packed_row(K, fmt)), _BYTES, dev)
-    _want("gamma", gamma, (1,), _ONLY_F32, dev)
-    _want("dx", dx, (M, K), _FLOATS, dev)
-    wp, wn = _workspace(ws, dev)
-    _call("bitlinear_backward_dx_bf16", dev, stream, packed.data_ptr(), fmt, gamma.data_ptr(), N, K, dz.data_ptr(), M,
-          dx.data_ptr(), _DT[dx.dtype], wp, wn)
+    status = (_native or _calls()).backward_dx_bf16(packed, fmt, gamma, N, K, dz, dx, ws, stream)
+    if status:
+        raise BitLinearError(status, "bitlinear_backward_dx_bf16")
 
 
 def bitlinear_backward_dw_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -412,38 +341,9 @@ def bitlinear_backward_dw_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
 
 def bitlinear_backward_dw_bf16(dz, xq, scale, gamma, dw, ws, stream=None) -> None:
     """dW = gamma dz^T x_deq on the tensor cores (bf16 dz, fp32 dW)."""
-    dev = _matrix("dz", dz)
-    M, N = dz.shape
-    K = xq.shape[-1]
-    _want("dz", dz, (M, N), _ONLY_BF16, dev)
-    _want("xq", xq, (M, K), _ONLY_I8, dev)
-    _want("scale", scale, (M,), _ONLY_F32, dev)
-    _want("gamma", gamma, (1,), _ONLY_F32, dev)
-    _want("dw", dw, (N, K), _ONLY_F32, dev)
-    wp, wn = _workspace(ws, dev)
-    _call("bitlinear_backward_dw_bf16", dev, stream, dz.data_ptr(), xq.data_ptr(), scale.data_ptr(), gamma.data_ptr(),
-          M, N, K, dw.data_ptr(), wp, wn)
-
-
-def _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
-                 pre_b, pre_eps):
-    if gate is not None and gate_rows < 1:
-        gate_rows = max(M, 1)       # one row for every token
-    row = (K,)
-    _want("post_w", post_w, row, _ONLY_F32, dev)
-    _want("post_b", post_b, row, _ONLY_F32, dev)
-    _want("pre_w", pre_w, row, _ONLY_F32, dev)
-    _want("pre_b", pre_b, row, _ONLY_F32, dev)
-    if gate is not None:
-        rows = -(-M // gate_rows)
-        if gate.dim() == 1:
-            _want("gate", gate, (K,), _ONLY_F32, dev)
-            if rows > 1:
-                raise ValueError(f"gate: one row, expected {rows}")
-        else:
-            _want("gate", gate, (rows, K), _ONLY_F32, dev)
-    return ResidualNormParams(post, post_eps, _raw(post_w), _raw(post_b), _raw(gate), gate_rows if gate is not None else 0,
-                              res_scale, branch_scale, pre, pre_eps, _raw(pre_w), _raw(pre_b))
+    status = (_native or _calls()).backward_dw_bf16(dz, xq, scale, gamma, dw, ws, stream)
+    if status:
+        raise BitLinearError(status, "bitlinear_backward_dw_bf16")
 
 
 def bitlinear_residual_norm(b, r, h, post=BL_NORM_NONE, post_w=None, post_b=None, post_eps=1e-5, gate=None,
@@ -452,18 +352,10 @@ def bitlinear_residual_norm(b, r, h, post=BL_NORM_NONE, post_w=None, post_b=None
     """h = res_scale r + branch_scale gate norm_post(b); y = norm_pre(h); xq, scale its INT8 codes.
 
     gate: [rows, K] with one row for every gate_rows tokens (0: one row for all, also as [K])."""
-    dev = _matrix("b", b)
-    M, K = b.shape
-    _want("b", b, (M, K), _FLOATS, dev)
-    _want("r", r, (M, K), _FLOATS, dev)
-    _want("h", h, (M, K), (r.dtype,), dev)
-    _want("y", y, (M, K), _FLOATS, dev)
-    _want("xq", xq, (M, K), _ONLY_I8, dev)
-    _want("scale", scale, (M,), _ONLY_F32, dev)
-    p = _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
-                     pre_b, pre_eps)
-    _call("bitlinear_residual_norm", dev, stream, C.addressof(p), b.data_ptr(), _DT[b.dtype], r.data_ptr(),
-          _DT[r.dtype], M, K, _raw(h), _raw(y), BL_F32 if y is None else _DT[y.dtype], _raw(xq), _raw(scale))
+    status = (_native or _calls()).residual_norm(b, r, h, post, post_w, post_b, post_eps, gate, gate_rows, res_scale,
+                                                 branch_scale, pre, pre_w, pre_b, pre_eps, y, xq, scale, stream)
+    if status:
+        raise BitLinearError(status, "bitlinear_residual_norm")
 
 
 def bitlinear_residual_norm_backward_workspace_bytes(M: int, K: int, gate_rows: int = 0) -> int:
@@ -476,26 +368,11 @@ def bitlinear_residual_norm_backward(dy, dh, b, h, dr, db, ws, post=BL_NORM_NONE
                                      pre=BL_NORM_RMS, pre_w=None, pre_eps=1e-5, dpost_w=None, dpost_b=None, dgate=None,
                                      dpre_w=None, dpre_b=None, stream=None) -> None:
     """Gradients of bitlinear_residual_norm from dy (of y) and dh (of h, or None)."""
-    dev = _matrix("dy", dy)
-    M, K = dy.shape
-    _want("dy", dy, (M, K), _FLOATS, dev)
-    _want("b", b, (M, K), _FLOATS, dev)
-    _want("h", h, (M, K), _FLOATS, dev)
-    _want("dh", dh, (M, K), (h.dtype,), dev)
-    _want("dr", dr, (M, K), (h.dtype,), dev)
-    _want("db", db, (M, K), (b.dtype,), dev)
-    for name, t in (("dpost_w", dpost_w), ("dpost_b", dpost_b), ("dpre_w", dpre_w), ("dpre_b", dpre_b)):
-        _want(name, t, (K,), _ONLY_F32, dev)
-    if dgate is not None:
-        if gate is None:
-            raise ValueError("dgate without a gate")
-        _want("dgate", dgate, tuple(gate.shape), _ONLY_F32, dev)
-    p = _norm_params(M, K, dev, post, post_w, post_b, post_eps, gate, gate_rows, res_scale, branch_scale, pre, pre_w,
-                     None, pre_eps)
-    g = ResidualNormGrads(_raw(dpost_w), _raw(dpost_b), _raw(dgate), _raw(dpre_w), _raw(dpre_b))
-    wp, wn = _workspace(ws, dev)
-    _call("bitlinear_residual_norm_backward", dev, stream, C.addressof(p), dy.data_ptr(), _DT[dy.dtype], _raw(dh),
-          b.data_ptr(), _DT[b.dtype], h.data_ptr(), _DT[h.dtype], M, K, _raw(dr), _raw(db), C.addressof(g), wp, wn)
+    status = (_native or _calls()).residual_norm_backward(dy, dh, b, h, dr, db, ws, post, post_w, post_b, post_eps,
+                                                          gate, gate_rows, res_scale, branch_scale, pre, pre_w, pre_eps,
+                                                          dpost_w, dpost_b, dgate, dpre_w, dpre_b, stream)
+    if status:
+        raise BitLinearError(status, "bitlinear_residual_norm_backward")
 
 
 def bitlinear_device_status(ws, stream=None) -> int:

@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` file is compiled to an object under ``_build/`` (in
 parallel), then linked with the static CUDA runtime into one shared library
 whose exported symbols are exactly the ``extern "C"`` functions of
-``include/bitlinear.h``.
+``include/bitlinear.h``.  ``csrc/bl_calls.cpp`` (the Python side of the calls made
+many times a step) is compiled with g++ against torch's headers into ``_calls.so``
+beside it.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libbitlinear.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -74,7 +77,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_calls(force)
     return LIB
+
+
+def _build_calls(force: bool = False) -> None:
+    """Compile csrc/bl_calls.cpp into _calls.so."""
+    src = os.path.join(CSRC, "bl_calls.cpp")
+    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "bitlinear.h")]):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    incs = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *(x for i in incs for x in ("-isystem", i)), src, "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-L", HERE, "-l:libbitlinear.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 if __name__ == "__main__":

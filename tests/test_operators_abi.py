@@ -43,8 +43,14 @@ def test_forward_epilogue_refusals(bl):
     assert call() == bl.BL_ERR_CUDA                   # passes every check: no device here
     assert call(bias=None, res=None, pre=None) == bl.BL_ERR_CUDA
     assert call(res=R) == bl.BL_ERR_CUDA              # in place
-    for a in ((1, 8640, 3200, 0, 1), (16, 3200, 8640, 1, 1), (4096, 8640, 3200, 2, 0)):
-        assert bl.bitlinear_forward_epilogue_workspace_bytes(*a) == bl.bitlinear_forward_workspace_bytes(*a)
+    q = bl.bitlinear_forward_epilogue_workspace_bytes
+    assert q(1, 8640, 3200, 0, 1) == 256              # the decode kernel
+    # 16 tokens in 16-byte pieces: 27 chunks of four 80-weight segments
+    assert q(16, 3200, 8640, 1, 1) == 256 + 27 * 4 * 80 * 16
+    # codes and int8 weights
+    assert q(4096, 8640, 3200, 2, 0) == 256 + 4096 * 3200 + 8640 * 3200
+    assert q(4096, 8640, 3200, 0, 2) == 256 + 8640 * 3200
+    assert q(0, 8640, 3200, 0, 1) == 256 and q(-1, 8, 8, 0, 1) == 0 and q(4, 8, 8, 3, 1) == 0
 
 
 def test_epilogue_backward_refusals(bl):
@@ -164,14 +170,33 @@ def test_binding_refuses_tensors(bl):
         bl.bitlinear_residual_norm(f, f, f)
     with pytest.raises(ValueError, match="dimensions"):
         bl.bitlinear_epilogue_backward(torch.zeros(4), None, 0, None, f, ws)
-    dev = f.device
-    with pytest.raises(TypeError, match="dtype"):
-        bl._want("y", f.half(), (4, 8), (torch.float32,), dev)
-    with pytest.raises(ValueError, match="shape"):
-        bl._want("y", f, (8, 4), (torch.float32,), dev)
-    with pytest.raises(ValueError, match="contiguous"):
-        bl._want("y", torch.zeros(8, 4).t(), (4, 8), (torch.float32,), dev)
-    with pytest.raises(ValueError, match="expected"):
-        bl._want("y", f.to("meta"), (4, 8), (torch.float32,), dev)
-    with pytest.raises(ValueError, match="one row"):
-        bl._norm_params(5, 8, dev, 1, None, None, 1e-5, torch.zeros(8), 2, 1.0, 1.0, 1, None, None, 1e-5)
+    y = torch.zeros(4, 8)
+    with pytest.raises(TypeError, match="h: unsupported dtype"):
+        bl.bitlinear_residual_norm(f, f, f.half())
+    with pytest.raises(ValueError, match="r: shape"):
+        bl.bitlinear_residual_norm(f, torch.zeros(8, 4), f)
+    with pytest.raises(ValueError, match="y must be contiguous"):
+        bl.bitlinear_residual_norm(f, f, f, y=torch.zeros(8, 4).t())
+    with pytest.raises(ValueError, match="one row, expected 2"):
+        bl.bitlinear_residual_norm(f, f, f, gate=torch.zeros(8), gate_rows=2)
+    with pytest.raises(ValueError, match="gate: shape"):
+        bl.bitlinear_residual_norm(f, f, f, gate=torch.zeros(3, 8), gate_rows=2)
+    with pytest.raises(ValueError, match="dgate without"):
+        bl.bitlinear_residual_norm_backward(f, None, f, f, f, f, ws, dgate=y)
+    with pytest.raises(ValueError, match="dh: shape"):
+        bl.bitlinear_residual_norm_backward(f, torch.zeros(4, 9), f, f, f, f, ws)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        bl.bitlinear_residual_norm(f, None, f)
+    codes, s = torch.zeros(16, 16, dtype=torch.uint8), torch.zeros(4)
+    with pytest.raises(ValueError, match="packed: shape"):
+        bl.bitlinear_forward_epilogue(codes, 0, torch.zeros(1), 16, 128, torch.zeros(4, 128), s, torch.zeros(4, 16), ws)
+    with pytest.raises(TypeError, match="residual: unsupported dtype"):
+        bl.bitlinear_forward_epilogue(codes, 0, torch.zeros(1), 16, 8, f, s, torch.zeros(4, 16), ws,
+                                      residual=torch.zeros(4, 16).bfloat16())
+    with pytest.raises(TypeError, match="dz: unsupported dtype"):
+        bl.bitlinear_backward_dw_bf16(f, torch.zeros(4, 8, dtype=torch.int8), s, torch.zeros(1), torch.zeros(8, 8), ws)
+    with pytest.raises(ValueError, match="dw: shape"):
+        bl.bitlinear_backward_dw_bf16(f.bfloat16(), torch.zeros(4, 8, dtype=torch.int8), s, torch.zeros(1),
+                                      torch.zeros(8, 9), ws)
+    with pytest.raises(ValueError, match="dx: shape"):
+        bl.bitlinear_backward_dx_bf16(codes[:8], 0, torch.zeros(1), 8, 8, f.bfloat16(), torch.zeros(4, 9), ws)
