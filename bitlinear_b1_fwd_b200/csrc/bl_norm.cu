@@ -816,10 +816,11 @@ int row_threads(int64_t K, int vec, int ni) {
   return static_cast<int>(((K + per - 1) / per + 31) / 32 * 32);
 }
 
-// Dynamic shared memory above the 48 KB that need no opt-in.
+// The opt-in for more than 48 KB of shared memory (the kernels' own 1 KB of sums
+// counts too).
 template <typename Kern>
 cudaError_t allow_smem(Kern kern, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
+  return bytes <= 44 * 1024 ? cudaSuccess
                             : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(bytes));
 }
@@ -924,14 +925,16 @@ cudaError_t launch_bwd(const NormParams& p, const void* dy, int dydt, const void
 
 }  // namespace
 
-// Row blocks of the backward (partial sums): what fits the SMs at some 832
-// threads each (64 registers a thread), eight blocks per SM at most.
+// Row blocks of the backward (partial sums): one wave of what the SMs hold at 112
+// registers a thread, eight blocks per SM at most (12000 x 1001: three blocks per
+// SM, of which two fit, took 126 us, two take 98).
 int64_t norm_grad_blocks(int64_t M, int64_t K) {
-  int64_t per_sm = 832 / row_threads(K, 4, 1);
+  const int threads = K % 8 == 0 ? row_threads(K, 8, K <= 8 * 512 ? 1 : 3) : row_threads(K, 1, K <= 4 * 512 ? 4 : 8);
+  int64_t per_sm = 576 / threads;
   per_sm = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
   const int64_t most = per_sm * device_sms();
-  const int64_t rows_per = (M + most - 1) / most;
-  return rows_per > 0 ? (M + rows_per - 1) / rows_per : 1;
+  int64_t rows_per = (M + most - 1) / most;
+  return M > 0 ? (M + rows_per - 1) / rows_per : 1;
 }
 
 cudaError_t launch_residual_norm(const NormParams& p, const void* b, int bdt, const void* r, int rdt, int64_t M,

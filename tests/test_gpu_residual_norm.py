@@ -286,6 +286,21 @@ def test_backward(M, K, post, pre):
                 assert torch.equal(some[k], got[k]), k
 
 
+@pytest.mark.parametrize("K", [2944, 3001, 4000, 5000, 7000, 8704, 9208])
+def test_widths_at_the_limits_of_shared_memory(K):
+    """Rows whose column vectors take about 48 KB (with and without a bias), and the longest that stay in registers."""
+    for bias in (True, False):
+        c = Case(5, K, BF16, BF16, RMS, LAYER, gate_rows=2, bias=bias, seed=30)
+        h64, eh, y64, ey = c.forward64()
+        h, y, _, _ = c.run(F32)
+        check(h, h64, eh + half_step(BF16) * (h64.abs() + eh) + 1e-38, "h")
+        check(y, y64, ey + 1e-38, "y")
+        want, got = Grads(c, h), backward(c, h)
+        for k, g in want.grad.items():
+            hs = half_step(got[k].dtype)
+            check(got[k], g, (want.tol[k] + 1e-38) * (1 + hs) + hs * g.abs(), f"d{k}")
+
+
 @pytest.mark.parametrize("M,K,gate_rows", [(1000, 64, 7), (301, 136, 301), (149, 48, 2), (148, 33, 148), (450, 20008, 100)])
 def test_gate_rows_and_blocks_of_tokens(M, K, gate_rows):
     """Runs of tokens with one gate row that begin and end inside blocks of tokens."""
