@@ -21,6 +21,7 @@
 // in registers over a block's rows and meet in a second kernel in a fixed order.
 // Statistics are two-pass (the mean, then the squares about it) in fp32.
 #include <atomic>
+#include <type_traits>
 
 #include "bl_common.cuh"
 #include "bl_gemv.cuh"
@@ -67,8 +68,16 @@ __device__ __forceinline__ float inv_dev(float sumsq, float rk, float eps) { ret
 // Column of value j of a thread's chunk i (VEC = 8: chunks of 8 neighbouring
 // columns; VEC = 1: neighbouring threads hold neighbouring columns).
 template <int VEC>
-__device__ __forceinline__ int64_t col0(int i) {
-  return (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * VEC;
+__device__ __forceinline__ int col0(int i) {  // (K <= 2^20)
+  return static_cast<int>((i * blockDim.x + threadIdx.x) * VEC);
+}
+
+// Row m of an array [.][K]: 64-bit arithmetic once per row and array, 32-bit
+// columns within (per access it was a third of the instructions of narrow rows).
+template <typename P>
+__device__ __forceinline__ P* row_of(P* p, int dt, int64_t m, int64_t K) {
+  using Byte = typename std::conditional<std::is_const<P>::value, const uint8_t, uint8_t>::type;
+  return reinterpret_cast<Byte*>(p) + m * K * (dt == BL_F32 ? 4 : 2);
 }
 
 // Per-column vectors folded once per block: vector v of chunk i of this thread,
@@ -144,21 +153,18 @@ __device__ __forceinline__ float dot_of(const Vals<VEC> (&v)[NI], const Vals<VEC
 
 // v - mean, zeros past K
 template <int VEC, int NI>
-__device__ __forceinline__ void centre(Vals<VEC> (&v)[NI], float mean, int64_t K) {
+__device__ __forceinline__ void centre(Vals<VEC> (&v)[NI], float mean, int W) {
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    if (col0<VEC>(i) < K)
-      v[i] = add(v[i], splat<VEC>(-mean));
-    else
-      v[i].fill(0.0f);
+    v[i] = add(v[i], splat<VEC>(col0<VEC>(i) < W ? -mean : 0.0f));
   }
 }
 
 // Normalises the row held in v (zeros past K) in place.
 template <int VEC, int NI>
-__device__ __forceinline__ void normalise(Vals<VEC> (&v)[NI], int kind, float eps, int64_t K, float rk, BlockSum& sum) {
+__device__ __forceinline__ void normalise(Vals<VEC> (&v)[NI], int kind, float eps, int W, float rk, BlockSum& sum) {
   if (kind == BL_NORM_NONE) return;
-  if (kind == BL_NORM_LAYER) centre<VEC, NI>(v, __fmul_rn(sum.one(sum_of<VEC, NI>(v)), rk), K);
+  if (kind == BL_NORM_LAYER) centre<VEC, NI>(v, __fmul_rn(sum.one(sum_of<VEC, NI>(v)), rk), W);
   const Vals<VEC> r = splat<VEC>(inv_dev(sum.one(dot_of<VEC, NI>(v, v)), rk, eps));
 #pragma unroll
   for (int i = 0; i < NI; ++i) v[i] = mul(v[i], r);
@@ -198,8 +204,9 @@ __device__ __forceinline__ uint2 quant8(const Vals<8>& v, float s, float c127) {
 
 // ---- forward, the row in registers --------------------------------------------
 // Up to 16 values per thread: the next row is in flight during this one, and the
-// column vectors sit in shared slots (0: gw, 1: w2, 2: gb, 3: b2); 32 values:
-// neither fits, the vectors are read again for each row.
+// column vectors sit in shared slots (0: gw, 1: w2, 2: gb, 3: b2; zeros past K, so
+// that only loads and stores ask whether a column exists); 32 values: neither
+// fits, the vectors are read again for each row.
 constexpr bool norm_hold(int values) { return values <= 16; }
 
 template <int BDT, int RDT, int VEC, int NI, bool BIAS>
@@ -214,18 +221,19 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC * NI <= 8 ? 2 :
   Slots<VEC, NI> slots{slot_mem};
   __shared__ __align__(16) float sum_mem[2][4][32];
   const float rk = __fdiv_rn(1.0f, static_cast<float>(K));
+  const int W = static_cast<int>(K);
   Raw<BDT, VEC> nb[NI];
   Raw<RDT, VEC> nr[NI];
   auto fetch = [&](int64_t m) {
+    const void *pb = row_of(b, BDT, m, K), *pr = row_of(r, RDT, m, K);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (m < M && k < K) {
-        nb[i].load(b, m * K + k);
-        nr[i].load(r, m * K + k);
-      } else {
-        nb[i].zero();
-        nr[i].zero();
+      const int k = col0<VEC>(i);
+      nb[i].zero();
+      nr[i].zero();
+      if (m < M && k < W) {
+        nb[i].load(pb, k);
+        nr[i].load(pr, k);
       }
     }
   };
@@ -236,21 +244,19 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC * NI <= 8 ? 2 :
   auto hold_branch = [&]() {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) {
-        slots.put(0, i, branch_factor<VEC>(p, gate, k));
-        if constexpr (BIAS) slots.put(2, i, branch_offset<VEC>(p, gate, k));
-      }
+      const int k = col0<VEC>(i);
+      const bool live = k < W;
+      slots.put(0, i, live ? branch_factor<VEC>(p, gate, k) : splat<VEC>(0.0f));
+      if constexpr (BIAS) slots.put(2, i, live ? branch_offset<VEC>(p, gate, k) : splat<VEC>(0.0f));
     }
   };
   if constexpr (kHold) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) {
-        slots.put(1, i, col_vals<VEC>(p.pre_w, k, 1.0f));
-        if constexpr (BIAS) slots.put(3, i, col_vals<VEC>(p.pre_b, k, 0.0f));
-      }
+      const int k = col0<VEC>(i);
+      const bool live = k < W;
+      slots.put(1, i, live ? col_vals<VEC>(p.pre_w, k, 1.0f) : splat<VEC>(0.0f));
+      if constexpr (BIAS) slots.put(3, i, live ? col_vals<VEC>(p.pre_b, k, 0.0f) : splat<VEC>(0.0f));
     }
     hold_branch();
   }
@@ -272,24 +278,26 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC * NI <= 8 ? 2 :
       gate = p.gate + g_row * K;
       if constexpr (kHold) hold_branch();
     }
-    normalise<VEC, NI>(v, p.post, p.post_eps, K, rk, sum);
+    void* ph = row_of(h, RDT, m, K);
+    normalise<VEC, NI>(v, p.post, p.post_eps, W, rk, sum);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) {
+      const int k = col0<VEC>(i);
+      if (kHold || k < W) {
         Vals<VEC> t = mul(rr[i], splat<VEC>(p.res_scale));
         if constexpr (BIAS) t = add(t, kHold ? slots.get(2, i) : branch_offset<VEC>(p, gate, k));
         v[i] = fma(kHold ? slots.get(0, i) : branch_factor<VEC>(p, gate, k), v[i], t);
-        if (h != nullptr) store_vals<RDT, VEC>(h, m * K + k, v[i]);
+        if (h != nullptr && k < W) store_vals<RDT, VEC>(ph, k, v[i]);
       }
     }
     if (y == nullptr && xq == nullptr) continue;
-    normalise<VEC, NI>(v, p.pre, p.pre_eps, K, rk, sum);
+    normalise<VEC, NI>(v, p.pre, p.pre_eps, W, rk, sum);
+    void* py = row_of(y, ydt, m, K);
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) {
+      const int k = col0<VEC>(i);
+      if (kHold || k < W) {
         const Vals<VEC> w = kHold ? slots.get(1, i) : col_vals<VEC>(p.pre_w, k, 1.0f);
         if constexpr (BIAS)
           v[i] = fma(v[i], w, kHold ? slots.get(3, i) : col_vals<VEC>(p.pre_b, k, 0.0f));
@@ -299,24 +307,25 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC * NI <= 8 ? 2 :
         v[i].get(f);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) amax = fmaxf(amax, fabsf(f[j]));
-        if (y != nullptr) store_vec_dt<VEC>(y, ydt, m * K + k, f);
+        if (y != nullptr && k < W) store_vec_dt<VEC>(py, ydt, k, f);
       }
     }
     if (xq == nullptr) continue;
     const float s = fmaxf(sum.max(amax), 1e-6f);
     const float c127 = __fdiv_rn(127.0f, s);
+    int8_t* pq = xq + m * K;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) {
+      const int k = col0<VEC>(i);
+      if (k < W) {
         if constexpr (VEC == 8) {
-          *reinterpret_cast<uint2*>(xq + m * K + k) = quant8(v[i], s, c127);
+          *reinterpret_cast<uint2*>(pq + k) = quant8(v[i], s, c127);
         } else {
           float f[VEC];
           int q[VEC];
           v[i].get(f);
           quant_act_fast_n<VEC>(f, s, c127, q);
-          xq[m * K + k] = static_cast<int8_t>(q[0]);
+          pq[k] = static_cast<int8_t>(q[0]);
         }
       }
     }
@@ -427,23 +436,25 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
   const int64_t plane = static_cast<int64_t>(gridDim.x) * K;
   bool grown = false;  // part holds dw1, db1 of earlier runs
   V aw2[kRegs], aA[kRegs], ab2[BIAS ? kRegs : 1], aB[BIAS ? kRegs : 1];
+  const int W = static_cast<int>(K);
   Raw<BDT, VEC> rb[NI];
   Raw<RDT, VEC> rh[NI], rg[NI];
   RawAny<VEC> gy[NI];
   auto fetch = [&](int64_t m) {
+    const void *pb = row_of(b, BDT, m, K), *ph = row_of(h, RDT, m, K), *pd = row_of(dh, RDT, m, K);
+    const void* py = row_of(dy, dydt, m, K);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
+      const int k = col0<VEC>(i);
       rg[i].zero();
-      if (m < m1 && k < K) {
-        rb[i].load(b, m * K + k);
-        rh[i].load(h, m * K + k);
-        gy[i].load(dy, dydt, m * K + k);
-        if (dh != nullptr) rg[i].load(dh, m * K + k);
-      } else {
-        rb[i].zero();
-        rh[i].zero();
-        gy[i].zero(dydt);
+      rb[i].zero();
+      rh[i].zero();
+      gy[i].zero(dydt);
+      if (m < m1 && k < W) {
+        rb[i].load(pb, k);
+        rh[i].load(ph, k);
+        gy[i].load(py, dydt, k);
+        if (dh != nullptr) rg[i].load(pd, k);
       }
     }
   };
@@ -455,8 +466,8 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
   auto hold_branch = [&]() {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) slots.put(0, i, branch_factor<VEC>(p, gate(), k));
+      const int k = col0<VEC>(i);
+      slots.put(0, i, k < W ? branch_factor<VEC>(p, gate(), k) : splat<VEC>(0.0f));
     }
   };
   // the sums of a finished run: into dw1, db1 and its gate row
@@ -465,8 +476,8 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
     float* dst = dgate == nullptr ? nullptr : whole ? dgate + g_row * K : gpart + (blockIdx.x + g_row) * K;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
-      if (k < K) {
+      const int k = col0<VEC>(i);
+      if (k < W) {
         V sA, sB;
         if constexpr (kInReg) {
           sA = aA[i];
@@ -513,7 +524,7 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
   };
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int64_t k = col0<VEC>(i);
+    const int k = col0<VEC>(i);
 #pragma unroll
     for (int v = 2; v < grad_slots(VEC * NI, BIAS); ++v) slots.put(v, i, splat<VEC>(0.0f));
     if constexpr (kInReg) {
@@ -524,7 +535,7 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
         aB[i].fill(0.0f);
       }
     }
-    if (k < K) slots.put(1, i, col_vals<VEC>(p.pre_w, k, 1.0f));
+    slots.put(1, i, k < W ? col_vals<VEC>(p.pre_w, k, 1.0f) : splat<VEC>(0.0f));
   }
   hold_branch();
   BlockSum sum(sum_mem);
@@ -551,49 +562,43 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
     }
     if (p.post == BL_NORM_LAYER || p.pre == BL_NORM_LAYER) {
       const float2 t = sum.two(sum_of<VEC, NI>(n1), sum_of<VEC, NI>(n2));
-      if (p.post == BL_NORM_LAYER) centre<VEC, NI>(n1, __fmul_rn(t.x, rk), K);
-      if (p.pre == BL_NORM_LAYER) centre<VEC, NI>(n2, __fmul_rn(t.y, rk), K);
+      if (p.post == BL_NORM_LAYER) centre<VEC, NI>(n1, __fmul_rn(t.x, rk), W);
+      if (p.pre == BL_NORM_LAYER) centre<VEC, NI>(n2, __fmul_rn(t.y, rk), W);
     }
     // both deviations, and the sums through the norm before the next block
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (col0<VEC>(i) < K)
-        d2[i] = mul(dyv[i], slots.get(1, i));
-      else
-        d2[i].fill(0.0f);
-    }
+    for (int i = 0; i < NI; ++i) d2[i] = mul(dyv[i], slots.get(1, i));
     const float4 t = sum.four(dot_of<VEC, NI>(n1, n1), dot_of<VEC, NI>(n2, n2), sum_of<VEC, NI>(d2),
                               dot_of<VEC, NI>(d2, n2));
     const float r1 = p.post == BL_NORM_NONE ? 1.0f : inv_dev(t.x, rk, p.post_eps);
     const float r2 = p.pre == BL_NORM_NONE ? 1.0f : inv_dev(t.y, rk, p.pre_eps);
     const float s = p.pre == BL_NORM_LAYER ? __fmul_rn(t.z, rk) : 0.0f;
     const float q = p.pre == BL_NORM_NONE ? 0.0f : __fmul_rn(__fmul_rn(r2, t.w), rk);
+    void *pr = row_of(dr, RDT, m, K), *po = row_of(db, BDT, m, K);
     const V r1v = splat<VEC>(r1), r2v = splat<VEC>(r2), mq = splat<VEC>(-q), ms = splat<VEC>(-s);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int64_t k = col0<VEC>(i);
+      const int k = col0<VEC>(i);
       n1[i] = mul(n1[i], r1v);
-      if (k < K) {
-        const V u2 = mul(n2[i], r2v);
-        d[i] = fma(r2v, fma(u2, mq, add(d2[i], ms)), d[i]);
-        if (dr != nullptr) store_vals<RDT, VEC>(dr, m * K + k, mul(splat<VEC>(p.res_scale), d[i]));
-        if constexpr (kInReg) {
-          aw2[i] = fma(dyv[i], u2, aw2[i]);
-          aA[i] = fma(d[i], n1[i], aA[i]);
-          if constexpr (BIAS) {
-            ab2[i] = add(ab2[i], dyv[i]);
-            aB[i] = add(aB[i], d[i]);
-          }
-        } else {
-          slots.put(kAcc, i, fma(dyv[i], u2, slots.get(kAcc, i)));
-          slots.put(kAcc + 1, i, fma(d[i], n1[i], slots.get(kAcc + 1, i)));
-          if constexpr (BIAS) {
-            slots.put(kAcc + 2, i, add(slots.get(kAcc + 2, i), dyv[i]));
-            slots.put(kAcc + 3, i, add(slots.get(kAcc + 3, i), d[i]));
-          }
+      const V u2 = mul(n2[i], r2v);
+      d[i] = fma(r2v, fma(u2, mq, add(d2[i], ms)), d[i]);
+      if (dr != nullptr && k < W) store_vals<RDT, VEC>(pr, k, mul(splat<VEC>(p.res_scale), d[i]));
+      if constexpr (kInReg) {
+        aw2[i] = fma(dyv[i], u2, aw2[i]);
+        aA[i] = fma(d[i], n1[i], aA[i]);
+        if constexpr (BIAS) {
+          ab2[i] = add(ab2[i], dyv[i]);
+          aB[i] = add(aB[i], d[i]);
         }
-        d2[i] = mul(slots.get(0, i), d[i]);  // dn1
-      }  // (d2 and n1 are zeros past K)
+      } else {
+        slots.put(kAcc, i, fma(dyv[i], u2, slots.get(kAcc, i)));
+        slots.put(kAcc + 1, i, fma(d[i], n1[i], slots.get(kAcc + 1, i)));
+        if constexpr (BIAS) {
+          slots.put(kAcc + 2, i, add(slots.get(kAcc + 2, i), dyv[i]));
+          slots.put(kAcc + 3, i, add(slots.get(kAcc + 3, i), d[i]));
+        }
+      }
+      d2[i] = mul(slots.get(0, i), d[i]);  // dn1
     }
     if (db != nullptr) {
       float s1 = 0.0f, p1 = 0.0f;
@@ -605,8 +610,8 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
       const V mp = splat<VEC>(-p1), m1v = splat<VEC>(-s1);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int64_t k = col0<VEC>(i);
-        if (k < K) store_vals<BDT, VEC>(db, m * K + k, mul(r1v, fma(n1[i], mp, add(d2[i], m1v))));
+        const int k = col0<VEC>(i);
+        if (k < W) store_vals<BDT, VEC>(po, k, mul(r1v, fma(n1[i], mp, add(d2[i], m1v))));
       }
     }
   }
@@ -614,8 +619,9 @@ __global__ void __launch_bounds__(grad_max_threads(VEC, NI))
   if (part == nullptr) return;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int64_t k = col0<VEC>(i), o = static_cast<int64_t>(blockIdx.x) * K + k;
-    if (k < K) {
+    const int k = col0<VEC>(i);
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * K + k;
+    if (k < W) {
       store_vals<BL_F32, VEC>(part, o, kInReg ? aw2[kInReg ? i : 0] : slots.get(kAcc, i));
       if constexpr (BIAS) store_vals<BL_F32, VEC>(part, o + plane, kInReg ? ab2[kInReg ? i : 0] : slots.get(kAcc + 2, i));
       if constexpr (kInReg) {
