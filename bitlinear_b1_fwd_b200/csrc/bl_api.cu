@@ -241,18 +241,19 @@ bl_status bitlinear_forward(const uint8_t* packed, int fmt, const float* gamma, 
 // The product with its epilogue has three forms: the decode kernels, the product
 // on packed weights (gemm_few) and the product on int8 weights (gemm_i8).
 //  - One token: the one-token decode kernel of the format where it takes the
-//    shape (3200 -> 8640: 5.6 us against 10.3), else gemm_few (512 -> 512 in base
-//    3: the general decode kernel takes 22.6 us, gemm_few 6.4).
+//    shape (3200 -> 8640: 5.5 us against 9.0), else gemm_few.  The base-3 decode
+//    kernel first fills a table, so small layers are gemm_few's (512 -> 512: 22.6
+//    us against 6.0; 3200 -> 3200: 7.0 and 7.0).
 //  - 2 to 4 tokens of 2-bit weights: the decode kernel's time grows with tokens,
-//    gemm_few's with the weights (2 tokens: 9.0 us against 10.3 for 3200 -> 8640,
-//    7.8 against 6.6 for 3200 -> 3200; 3 tokens: 26.6 against 36.9 for 8192 ->
-//    28672, 14.1 against 11.5 for 8640 -> 3200).
+//    gemm_few's with the weights (2 tokens: 8.9 us against 9.0 for 3200 -> 8640,
+//    7.8 against 5.8 for 3200 -> 3200; 3 tokens: 26.7 against 30.3 for 8192 ->
+//    28672, 14.1 against 9.3 for 8640 -> 3200).
 //  - Up to 64 tokens, MB of them in groups of 8, 16, 32 or 64: gemm_few takes some
-//    3 us + (2 + MB / 20 + 0.6 K / 1000) us for each turn of its blocks of 16 rows
-//    on the SMs (two fit up to MB = 16), gemm_i8 some 11 us (8 more for odd rows)
-//    + 2.6 NK / 10^7 us (writing and reading the int8 weights) + 0.27 us a k-block
-//    of the busiest SM pair (16 tokens, 3200 -> 8640: 15.4 us against 24.4; 64
-//    tokens: 31.1 against 23.0; 64 tokens, 8192 -> 8192: 36.4 against 43.6).
+//    3 us + (1.5 + MB / 20 + 0.45 K / 1000) us for each turn of its blocks of 16
+//    rows on the SMs (two fit up to MB = 16), gemm_i8 some 11 us (8 more for odd
+//    rows) + 2.6 NK / 10^7 us (writing and reading the int8 weights) + 0.27 us a
+//    k-block of the busiest SM pair (16 tokens, 3200 -> 8640: 13.0 us against 24.4;
+//    64 tokens: 31 against 21.3; 64 tokens, 8192 -> 8192: 38 against 43.6).
 enum class ForwardPath { kGemv, kFew, kMany };
 static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K, int fmt, int xdt) {
   const int64_t rb = bitlinear_packed_row_bytes(K, fmt);
@@ -261,7 +262,7 @@ static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K, int fmt, int x
     const bool fits = fmt == BL_PACK_I2   ? bl::gemv1_fits(N, K, rb, xdt)
                       : fmt == BL_PACK_T5 ? bl::gemv1_t5_fits(N, K, rb, xdt)
                                           : bl::gemv1_b1_fits(N, K, rb, xdt);
-    return fits ? ForwardPath::kGemv : ForwardPath::kFew;
+    return fits && (fmt != BL_PACK_T5 || nk >= 0.84) ? ForwardPath::kGemv : ForwardPath::kFew;
   }
   if (M <= bl::kGemvMaxTokens && fmt == BL_PACK_I2 && bl::gemv_max_tokens(fmt, rb) >= 1 &&
       nk * 1e7 >= static_cast<double>(int64_t{1} << (20 + 2 * M)))
@@ -270,7 +271,7 @@ static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K, int fmt, int x
   const int64_t tiles = (N + 255) / 256, ks = bl::gemm_i8_parts(M, N, K), pairs = bl::device_sms() / 2;
   const double mb = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
   const int64_t fit = bl::device_sms() * (mb <= 16 ? 2 : 1), turns = ((N + 15) / 16 + fit - 1) / fit;
-  const double few = 3 + static_cast<double>(turns) * (2 + mb / 20 + 0.0006 * static_cast<double>(K));
+  const double few = 3 + static_cast<double>(turns) * (1.5 + mb / 20 + 0.00045 * static_cast<double>(K));
   const double many = 11 + (N % 8 != 0 || K % 16 != 0 ? 8 : 0) + 2.6 * nk +
                       0.27 * static_cast<double>((tiles * ks + pairs - 1) / pairs * ((K + 127) / 128 / ks));
   return few <= many ? ForwardPath::kFew : ForwardPath::kMany;

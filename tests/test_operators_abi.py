@@ -45,8 +45,8 @@ def test_forward_epilogue_refusals(bl):
     assert call(res=R) == bl.BL_ERR_CUDA              # in place
     q = bl.bitlinear_forward_epilogue_workspace_bytes
     assert q(1, 8640, 3200, 0, 1) == 256              # the decode kernel
-    # 16 tokens in 16-byte pieces: 27 chunks of four 80-weight segments
-    assert q(16, 3200, 8640, 1, 1) == 256 + 27 * 4 * 80 * 16
+    # 16 tokens in 16-byte pieces: 27 chunks of four 80-weight segments, and a sum each
+    assert q(16, 3200, 8640, 1, 1) == 256 + 27 * 4 * 80 * 16 + 16 * 4
     # codes and int8 weights
     assert q(4096, 8640, 3200, 2, 0) == 256 + 4096 * 3200 + 8640 * 3200
     assert q(4096, 8640, 3200, 0, 2) == 256 + 8640 * 3200
