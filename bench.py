@@ -969,6 +969,7 @@ PROFILE_CASES = {
     "quantize_3b_up_t5": dict(N=8640, K=3200, fmt=1, M=1, sigma=0.02, op="quantize"),
     "train_3b_up": dict(N=8640, K=3200, fmt=0, M=4096, sigma=0.02, op="train"),
     "train_3b_odd_m130": dict(N=3201, K=3200, fmt=0, M=130, sigma=0.02, op="train"),
+    "train_3b_down_m16_t5": dict(N=3200, K=8640, fmt=1, M=16, sigma=0.02, op="train"),
     "norm_3b": dict(N=64, K=3200, fmt=0, M=4096, sigma=0.02, op="norm"),
     "norm_70b_down": dict(N=64, K=28672, fmt=0, M=512, sigma=0.01, op="norm"),
 }

@@ -129,6 +129,46 @@ def test_forward_epilogue(orc, M, N, K, fmt, xdt, ydt):
             check(z, z64, tz, "z")
 
 
+# every form at its edges: the packed-weight product at one token and at 8, 16, 32 and 64, K over several parts of
+# codes, one token group shared by several warps; the int8 product whole and with K in parts, rows of y and of x that
+# are no multiple of 16 bytes, one tile and several; the decode kernels at two tokens
+EDGES = [(1, 512, 512, T5), (1, 40, 1011, B1), (2, 8640, 3200, I2), (3, 1040, 77, B1), (8, 16, 16, I2), (16, 17, 9000, I2),
+         (32, 50, 12000, T5), (33, 33, 20000, B1), (64, 40, 40, T5), (64, 3200, 3200, I2), (65, 777, 1011, B1),
+         (65, 96, 4096, I2), (130, 3200, 640, T5), (257, 264, 130, I2), (600, 777, 1011, T5), (1030, 1000, 72, B1)]
+
+
+@pytest.mark.parametrize("M,N,K,fmt", EDGES)
+def test_forward_epilogue_at_the_edges_of_its_forms(orc, M, N, K, fmt):
+    L = Layer(orc, N, K, fmt, 960 + K)
+    bias = dev(synth.normal_f32(961, (N,), 0.3))
+    x32 = dev(synth.normal_f32(962 + M, (M, K)))
+    for act, xdt, ydt in ((B.BL_ACT_SILU, BF16, BF16), (B.BL_ACT_GELU, F32, F32), (B.BL_ACT_GELU, BF16, BF16)):
+        x = x32.to(xdt)
+        res = dev(synth.normal_f32(963 + M, (M, N))).to(ydt)
+        y, z, s = L.run(x, ydt, bias, act, res, True)
+        main, z64, y64, xq, s_ref = L.reference(x, bias, act, res)
+        assert np.array_equal(host(s), s_ref)
+        tz, ty = bounds(main, z64, y64, act, ydt)
+        check(y, y64, ty, "y")
+        check(z, z64, tz, "z")
+        given, zg, _ = L.run(dev(xq), ydt, bias, act, res, True, scale=dev(s_ref))      # codes instead of x
+        assert torch.equal(given, y) and torch.equal(zg, z)
+
+
+def test_two_calls_at_once(orc):
+    """Two streams, each with its own workspace and outputs."""
+    for M, N, K, fmt in ((12, 1000, 2048, T5), (300, 777, 640, I2)):
+        L = Layer(orc, N, K, fmt, 970)
+        xs = [dev(synth.normal_f32(971 + i, (M, K))).to(BF16) for i in range(2)]
+        want = [L.run(x, BF16, None, B.BL_ACT_SILU)[0] for x in xs]
+        torch.cuda.synchronize()
+        streams, got = [torch.cuda.Stream() for _ in range(2)], []
+        for _ in range(4):
+            got.append([L.run(x, BF16, None, B.BL_ACT_SILU, stream=st)[0] for x, st in zip(xs, streams)])
+            torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for pair in got for a, b in zip(pair, want))
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M", [1, 3, 20, 140])
 def test_every_activation(orc, M, act):
