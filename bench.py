@@ -72,7 +72,7 @@ KERNEL_SOURCE = {"absmean_kernel": "bl_weights.cu", "ternarize_flat_kernel": "bl
                  "i2_to_bf16_kernel": "bl_gemm_grad.cu", "pad_rows_kernel": "bl_gemm_grad.cu",
                  "grad_max_kernel": "bl_gemm_grad.cu", "grad_split_kernel": "bl_gemm_grad.cu",
                  "gemm_i8_kernel": "bl_gemm_i8.cu",
-                 "gemm_parts_kernel": "bl_gemm_i8.cu", "gemm_few_kernel": "bl_gemm_few.cu", "act_pieces_kernel": "bl_gemm_few.cu",
+                 "gemm_parts_kernel": "bl_gemm_i8.cu", "dx_few_kernel": "bl_dx_few.cu", "gemm_few_kernel": "bl_gemm_few.cu", "act_pieces_kernel": "bl_gemm_few.cu",
                  "gemm_operands_kernel": "bl_gemm_i8.cu",
                  "residual_norm_kernel": "bl_norm.cu", "residual_norm_long_kernel": "bl_norm.cu",
                  "residual_norm_grad_kernel": "bl_norm.cu", "residual_norm_grad_stats_kernel": "bl_norm.cu",

@@ -503,8 +503,13 @@ bl_status bitlinear_epilogue_backward(const void* dy, int dydt, const void* z, i
 size_t bitlinear_backward_dx_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt) {
   if (N < 1 || !m_ok(M) || !nk_ok(N, K) || !fmt_ok(fmt)) return 0;
   const int64_t rb2 = bitlinear_packed_row_bytes(K, BL_PACK_I2);
-  size_t bytes = BL_WS_HEADER_BYTES + round256(static_cast<size_t>(N) * bl::grad_ld(K) * 2);
+  size_t bytes = BL_WS_HEADER_BYTES;
   if (fmt != BL_PACK_I2) bytes += round256(static_cast<size_t>(N) * rb2);
+  if (bl::dx_few_fits(M, N)) {
+    const int64_t parts = bl::dx_few_parts(N, K);
+    return parts > 1 ? bytes + round256(static_cast<size_t>(parts) * M * K * sizeof(float)) : bytes;
+  }
+  bytes += round256(static_cast<size_t>(N) * bl::grad_ld(K) * 2);
   if (N % 8 != 0) bytes += round256(static_cast<size_t>(M) * bl::grad_ld(N) * 2);
   const int ks = bl::grad_dx_parts(M, N, K);
   if (ks > 1) bytes += round256(static_cast<size_t>(ks) * M * K * sizeof(float));
@@ -533,6 +538,9 @@ bl_status bitlinear_backward_dx_bf16(const uint8_t* packed, int fmt, const float
     w2 = scratch;
     scratch += round256(static_cast<size_t>(N) * rb2);
   }
+  if (bl::dx_few_fits(M, N))
+    return cuda_status(bl::launch_dx_few(w2, rb2, static_cast<const uint16_t*>(dz), gamma, M, N, K, dx, dxdt,
+                                         reinterpret_cast<float*>(scratch), st));
   const int64_t ldw = bl::grad_ld(K);
   uint16_t* w16 = reinterpret_cast<uint16_t*>(scratch);
   if (bl::launch_i2_to_bf16(w2, N, rb2, w16, st) != cudaSuccess) return BL_ERR_CUDA;

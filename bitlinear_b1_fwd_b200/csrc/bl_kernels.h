@@ -147,6 +147,14 @@ cudaError_t launch_pad_rows(const uint16_t* src, int64_t M, int64_t N, int64_t l
 cudaError_t launch_grad_dx(const uint16_t* dz, int64_t lddz, const uint16_t* w, int64_t ldw, const float* gamma,
                            int64_t M, int64_t N, int64_t K, void* dx, int dxdt, float* part, void* ws,
                            cudaStream_t st);
+// out = gamma times the ks parts of n values, added in order.
+cudaError_t launch_grad_parts(const float* part, int ks, int64_t n, const float* gamma, void* out, int odt,
+                              cudaStream_t st);
+// dx of a few tokens from 2-bit rows; part: [dx_few_parts(N, K)][M][K] when more than one.
+bool dx_few_fits(int64_t M, int64_t N);
+int64_t dx_few_parts(int64_t N, int64_t K);
+cudaError_t launch_dx_few(const uint8_t* packed, int64_t rowbytes, const uint16_t* dz, const float* gamma, int64_t M,
+                          int64_t N, int64_t K, void* dx, int dxdt, float* part, cudaStream_t st);
 struct GradDwScratch {
   uint32_t* maxes;  // [grad_rowmax_ranges(M, N)][N]
   float* rowinv;    // [N]

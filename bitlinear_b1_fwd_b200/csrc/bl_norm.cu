@@ -20,6 +20,9 @@
 // for the codes' maximum; backward two).  The column sums of the backward stay
 // in registers over a block's rows and meet in a second kernel in a fixed order.
 // Statistics are two-pass (the mean, then the squares about it) in fp32.
+// 4096 x 3200 bf16, RMS + RMS: forward 23 us with bf16 y (floor 16), gradient 49 us
+// (floor 24: 13 warps an SM, latency-bound); 12000 x 1001, one column per lane, 46
+// and 74 us (floors 15 and 22: instructions).
 #include <atomic>
 #include <type_traits>
 
@@ -33,7 +36,7 @@ namespace {
 
 // Threads of a block, by chunks and values per thread: what its registers allow.
 constexpr int norm_max_threads(int vec, int ni) { return vec == 8 && ni == 2 ? 576 : 512; }
-constexpr int grad_max_threads(int vec, int ni) { return vec == 8 && ni == 1 || ni == 4 ? 512 : vec == 4 ? 1024 : 384; }
+constexpr int grad_max_threads(int vec, int ni) { return vec == 8 && ni == 1 || ni == 4 ? 512 : 384; }
 constexpr int kNormLongThreads = 512;
 constexpr size_t kGradSmemBudget = 225 * 1024;  // slots of the backward
 

@@ -39,31 +39,6 @@ struct Raw<BL_F32, 8> {
   }
 };
 template <>
-struct Raw<BL_BF16, 4> {
-  uint2 q;
-  __device__ __forceinline__ void zero() { q = make_uint2(0, 0); }
-  __device__ __forceinline__ void load(const void* p, int64_t e) {
-    q = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + e));
-  }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = __uint_as_float(q.x << 16);
-    v[1] = __uint_as_float(q.x & 0xffff0000u);
-    v[2] = __uint_as_float(q.y << 16);
-    v[3] = __uint_as_float(q.y & 0xffff0000u);
-  }
-};
-template <>
-struct Raw<BL_F32, 4> {
-  float4 a;
-  __device__ __forceinline__ void zero() { a = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-  __device__ __forceinline__ void load(const void* p, int64_t e) {
-    a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + e));
-  }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  }
-};
-template <>
 struct Raw<BL_F32, 1> {
   float f;
   __device__ __forceinline__ void zero() { f = 0.0f; }
@@ -88,8 +63,8 @@ struct RawAny {
   __device__ __forceinline__ void get(int dt, float* v) const { dt == BL_F32 ? f.get(v) : h.get(v); }
 };
 
-// VEC consecutive elements from element e (VEC = 8, 4: e a multiple of it and
-// the array 16-byte aligned; VEC = 1: any), widened to fp32.
+// VEC consecutive elements from element e (VEC = 8: e a multiple of 8 and the
+// array 16-byte aligned; VEC = 1: any), widened to fp32.
 template <int DT, int VEC>
 __device__ __forceinline__ void load_vec(const void* p, int64_t e, float* v) {
   if constexpr (VEC == 8) {
@@ -97,10 +72,6 @@ __device__ __forceinline__ void load_vec(const void* p, int64_t e, float* v) {
     load8_aligned<DT>(p, e, t);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = t[j];
-  } else if constexpr (VEC == 4) {
-    Raw<DT, 4> r;
-    r.load(p, e);
-    r.get(v);
   } else {
     v[0] = load_elem<DT>(p, e);
   }
@@ -125,8 +96,6 @@ __device__ __forceinline__ void store_vec(void* p, int64_t e, const float* v) {
     if constexpr (VEC == 8) {
       reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(q)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if constexpr (VEC == 4) {
-      reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
     } else {
       q[0] = v[0];
     }
@@ -134,8 +103,6 @@ __device__ __forceinline__ void store_vec(void* p, int64_t e, const float* v) {
     if constexpr (VEC == 8) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e) =
           make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
-    } else if constexpr (VEC == 4) {
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + e) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     } else {
       static_cast<__nv_bfloat16*>(p)[e] = __float2bfloat16_rn(v[0]);
     }

@@ -297,7 +297,10 @@ BL_API bl_status bitlinear_backward_dw(const void *dy, int dydt, const int8_t *x
  *   y[m, n] = act(z[m, n]) + residual[m, n]     (fp32, one rounding to ydt),
  * with acc and c_m as in bitlinear_forward.  z does not depend on M or on the
  * kernel that serves the sizes (acc is an exact integer, c_m z two fp32
- * roundings): a token gives the same y alone and in a batch.
+ * roundings): a token gives the same y alone and in a batch.  SiLU and GELU
+ * are within 8 u |act| of the formula for fp32 y (GELU and a few u z^2 |act|; u =
+ * 2^-24), and within 2^-17 |act| before the rounding for bf16 y, where results
+ * below 2^-119 become 0.
  *   packed, fmt, gamma, x, xdt, scale  as for bitlinear_forward.
  *   bias      [N] fp32, or NULL (0).
  *   act       bl_act; BL_ACT_GELU is z Phi(z) with the error function.
@@ -305,7 +308,10 @@ BL_API bl_status bitlinear_backward_dw(const void *dy, int dydt, const int8_t *x
  *   preact    [M, N] of type ydt: receives z for the backward pass, or NULL;
  *             must not overlap y or residual.
  *   y         [M, N] BL_F32 or BL_BF16.
- *   ws        at least bitlinear_forward_epilogue_workspace_bytes(...). */
+ *   ws        at least bitlinear_forward_epilogue_workspace_bytes(...): one
+ *             token's decode kernels need the header only, batches of up to
+ *             64 tokens a copy of their codes, larger ones the codes, the
+ *             weights as int8 (N K bytes) and, with few tiles, INT32 parts. */
 typedef enum {
   BL_ACT_NONE = 0,
   BL_ACT_RELU = 1,
@@ -343,12 +349,12 @@ BL_API bl_status bitlinear_epilogue_backward(const void *dy, int dydt, const voi
  *       entry is near 2^13), times the exact x_q.
  * Both add runs of contracted elements (512 for dx, 256 for dW) on the tensor
  * core in fp32 and the runs in fp32 registers in order: the same bits on every
- * call.  The error is below 2^-16 sum |terms| (at most 32 truncating additions
- * a run).
+ * call (dx of up to 32 tokens: runs of the same length on another kernel).  The
+ * error is below 2^-16 sum |terms| (at most 32 truncating additions a run).
  *   packed, fmt, gamma  as for bitlinear_forward.
  *   dx   [M, K] BL_F32 or BL_BF16;  dw [N, K] fp32 (zeros when M is 0).
  *   xq, scale           the forward's codes and scales.
- *   ws   at least the query's size (dx: a bf16 copy of the codes, N K 2 bytes;
+ *   ws   at least the query's size (dx of more than 32 tokens: a bf16 copy of the codes, N K 2 bytes;
  *        dW: two fp16 planes of dz and one of x_q). */
 BL_API size_t bitlinear_backward_dx_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt);
 BL_API bl_status bitlinear_backward_dx_bf16(const uint8_t *packed, int fmt, const float *gamma, int64_t N, int64_t K,

@@ -107,6 +107,19 @@ def test_products(orc, M, N, K, fmt):
     assert torch.equal(c.dx(), c.dx()) and torch.equal(c.dw(), c.dw())
 
 
+# up to 32 tokens take packed weights: row counts on and off the step of 16, columns on and off the block of 128,
+# one range of rows and several, more rows than one warp adds up, every format; 33 tokens do not
+@pytest.mark.parametrize("M,N,K,fmt", [(1, 15, 129, I2), (8, 16, 128, I2), (16, 4097, 96, I2), (17, 333, 1000, T5),
+                                       (32, 9000, 40, I2), (31, 8640, 320, B1), (5, 40000, 130, I2), (32, 100, 5000, T5),
+                                       (33, 100, 500, T5)])
+def test_dx_of_a_few_tokens(orc, M, N, K, fmt):
+    c = Case(orc, M, N, K, fmt, 1300 + M)
+    f, b = c.dx(F32), c.dx(BF16)
+    c.check_dx(f)
+    c.check_dx(b)
+    assert torch.equal(c.dx(F32), f) and torch.equal(f.to(BF16), b)
+
+
 @pytest.mark.parametrize("M,N,K", [(200, 300, 264), (70, 129, 64)])
 def test_gradients_of_very_different_size(orc, M, N, K):
     """Each output row of dW has its own power of two: rows 2^-60 .. 2^60 apart keep their precision."""
