@@ -264,7 +264,7 @@ static ForwardPath epilogue_path(int64_t M, int64_t N, int64_t K, int fmt, int x
                                           : bl::gemv1_b1_fits(N, K, rb, xdt);
     return fits && (fmt != BL_PACK_T5 || nk >= 0.84) ? ForwardPath::kGemv : ForwardPath::kFew;
   }
-  if (M <= bl::kGemvMaxTokens && fmt == BL_PACK_I2 && bl::gemv_max_tokens(fmt, rb) >= 1 &&
+  if (M <= bl::kGemvMaxTokens && fmt == BL_PACK_I2 && bl::gemv_epilogue_fits(M, N, rb) &&
       nk * 1e7 >= static_cast<double>(int64_t{1} << (20 + 2 * M)))
     return ForwardPath::kGemv;
   if (M > bl::kFewTokens) return ForwardPath::kMany;

@@ -381,7 +381,6 @@ quant_act_fast_n<8>(e, s_tok[m], c127, q);
       consume(bufB);
     }
     __syncthreads();  // every part of every row of the tile has been added
-    const Epilogue ep = epilogue_after_wait(rg.ep);
     for (int r = threadIdx.x; r < static_cast<int>(nr); r += blockDim.x) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -389,7 +388,12 @@ quant_act_fast_n<8>(e, s_tok[m], c127, q);
         racc[m * kGemvTileRows + r] = 0;
         const int64_t o = m * N + row0 + t0 + r;
         const float cf = rg.n == 1 ? cfac[m] : dequant_factor(sh_gam[row_group(rg, row0 + t0 + r)], s_tok[m]);
-        epilogue_store(ep, y, ydt, o, row0 + t0 + r, a, cf);
+        if (ydt == BL_I32)
+          static_cast<int32_t*>(y)[o] = a;
+        else if (ydt == BL_F32)
+          static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
+        else
+          static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
       }
     }
     __syncthreads();  // the row sums are zero again for the next tile
@@ -840,7 +844,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       }
     }
     __syncthreads();  // every part of every row of the tile has been added
-    const Epilogue ep = epilogue_after_wait(rg.ep);
     for (int r = threadIdx.x; r < static_cast<int>(nr); r += blockDim.x) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -848,7 +851,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         racc[m * kGemvTileRows + r] = 0;
         const int64_t o = m * N + row0 + t0 + r;
         const float cf = rg.n == 1 ? cfac[m] : dequant_factor(sh_gam[row_group(rg, row0 + t0 + r)], s_tok[m]);
-        epilogue_store(ep, y, ydt, o, row0 + t0 + r, a, cf);
+        if (ydt == BL_I32)
+          static_cast<int32_t*>(y)[o] = a;
+        else if (ydt == BL_F32)
+          static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
+        else
+          static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
       }
     }
     __syncthreads();  // the row sums are zero again for the next tile
@@ -877,7 +885,8 @@ __host__ __device__ inline int64_t gemv_mt_smem_bytes(int64_t rowbytes, int mt) 
   return int64_t{4} * rowbytes * mt + int64_t{4} * kGemvTileRows * mt;  // codes | row sums
 }
 
-template <int MT, int XDT>
+// EP: with an epilogue (the plain kernel keeps its registers).
+template <int MT, int XDT, bool EP>
 __global__ void __launch_bounds__(kMtThreads, 1)
     gemv_i2_mt_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                       int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
@@ -1068,14 +1077,20 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     }
   }
   __syncthreads();  // every part of every row has been added
-  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = threadIdx.x; r < nrows; r += nthr) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int a = racc[m * kGemvTileRows + r] - corr[m];
       const int64_t o = m * N + row0 + r;
       const float cf = rg.n == 1 ? cfac[m] : dequant_factor(sh_gam[row_group(rg, row0 + r)], s_tok[m]);
-      epilogue_store(ep, y, ydt, o, row0 + r, a, cf);
+      if constexpr (EP)
+        epilogue_store(epilogue_after_wait(rg.ep), y, ydt, o, row0 + r, a, cf);
+      else if (ydt == BL_I32)
+        static_cast<int32_t*>(y)[o] = a;
+      else if (ydt == BL_F32)
+        static_cast<float*>(y)[o] = __fmul_rn(__int2float_rn(a), cf);
+      else
+        static_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
     }
   }
 }
@@ -1400,7 +1415,7 @@ template <int MT, int XDT>
 static cudaError_t launch_gemv_mt_cs(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N,
                                      int64_t K, const void* x, float* scale, void* y, int ydt, int write_scale,
                                      const RowGroups& rg, cudaStream_t st) {
-  auto kern = gemv_i2_mt_kernel<MT, XDT>;
+  auto kern = rg.ep.act >= 0 ? gemv_i2_mt_kernel<MT, XDT, true> : gemv_i2_mt_kernel<MT, XDT, false>;
   const size_t smem = static_cast<size_t>(gemv_mt_smem_bytes(rowbytes, MT));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -1460,10 +1475,15 @@ static cudaError_t launch_gemv_mt(int mt, const uint8_t* packed, int64_t rowbyte
   }
 }
 
+// M tokens of 2-bit rows with an epilogue: the column-stationary kernel in one launch.
+bool gemv_epilogue_fits(int64_t M, int64_t N, int64_t rowbytes) {
+  return M >= 2 && M <= gemv_max_tokens(BL_PACK_I2, rowbytes) && gemv_mt_fits(rowbytes, N, static_cast<int>(M));
+}
+
 // Runs the GEMV over all M tokens in groups that fit in shared memory.
 cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
                         const void* x, int xdt, float* scale, int64_t M, void* y, int ydt,
-                        const RowGroups& rg_all, void* ws, cudaStream_t st) {
+                        const RowGroups& rg, void* ws, cudaStream_t st) {
   const int per = (fmt == BL_PACK_I2) ? 4 : (fmt == BL_PACK_T5 ? 5 : 8);
   const int64_t rowbytes = ((K + per - 1) / per + 15) / 16 * 16;
   const int mt_max = gemv_max_tokens(fmt, rowbytes);
@@ -1475,11 +1495,11 @@ cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int6
   const bool lean = (fmt == BL_PACK_I2 && rowbytes <= 2 * kI2Plane) || (fmt == BL_PACK_B1 && rowbytes <= kI2Plane);
   if (fmt == BL_PACK_B1 && !lean) return cudaErrorInvalidValue;
   if (fmt == BL_PACK_I2 && M == 1 && gemv1_fits(N, K, rowbytes, xdt))
-    return launch_gemv1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg_all, ws, st);
+    return launch_gemv1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
   if (fmt == BL_PACK_T5 && M == 1 && gemv1_t5_fits(N, K, rowbytes, xdt))
-    return launch_gemv1_t5(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg_all, ws, st);
+    return launch_gemv1_t5(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
   if (fmt == BL_PACK_B1 && M == 1 && gemv1_b1_fits(N, K, rowbytes, xdt))
-    return launch_gemv1_b1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg_all, ws, st);
+    return launch_gemv1_b1(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
   const int esz = (xdt == BL_F32) ? 4 : (xdt == BL_BF16 ? 2 : 1);
   const int ysz = (ydt == BL_BF16) ? 2 : 4;
   for (int64_t m0 = 0; m0 < M; m0 += mt_max) {
@@ -1487,9 +1507,6 @@ cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int6
     const void* xm = static_cast<const uint8_t*>(x) + m0 * K * esz;
     float* sm = scale + m0;
     void* ym = static_cast<uint8_t*>(y) + m0 * N * ysz;
-    RowGroups rg = rg_all;  // the residual and the kept pre-activation start at these tokens too
-    if (rg.ep.res != nullptr) rg.ep.res = static_cast<const uint8_t*>(rg.ep.res) + m0 * N * ysz;
-    if (rg.ep.pre != nullptr) rg.ep.pre = static_cast<uint8_t*>(rg.ep.pre) + m0 * N * ysz;
     cudaError_t e;
     if (fmt == BL_PACK_I2 && mt >= 2 && mt <= 4 && gemv_mt_fits(rowbytes, N, mt)) {
       if (xdt == BL_F32) e = launch_gemv_mt_cs_n<BL_F32>(mt, packed, rowbytes, gamma, N, K, xm, sm, ym, ydt, 1, rg, st);

@@ -29,6 +29,8 @@
 // point of coherence, so the loads after the wait still see whatever the
 // previous kernel writes).  After the wait it reads the token, quantizes it
 // and streams its rows with D 16-byte loads in flight per thread.
+#include <type_traits>
+
 #include "bl_common.cuh"
 #include "bl_epilogue.cuh"
 #include "bl_gemv.cuh"
@@ -161,7 +163,7 @@ __device__ __forceinline__ uint4 g1_codes16(const float (&e)[16], float s, float
 // XC: 16-element chunks of the token per thread (the chunks of segment c are
 // 4c .. 4c + 3; chunk g of thread t is t + T u, u < XC).  S: stages of the
 // thread's row ring.  ALIGNED: segs % 32 == 0, so every warp lies in one row.
-template <int XDT, int XC, int S, bool ALIGNED>
+template <int XDT, int XC, int S, bool ALIGNED, bool EP>
 __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
     gemv1_i2_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                     int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
@@ -403,7 +405,6 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
 
   // 6. dequantize and store the CTA's outputs (coalesced)
   const float cf1 = dequant_factor(sh_gam[0], s);
-  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = tid; r < nrows; r += T) {
     const int a = rsum[r];
     const int64_t n = row0 + r;
@@ -413,7 +414,14 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
       while (gi + 1 < rg.n && n >= sh_end[gi]) ++gi;
       cf = dequant_factor(sh_gam[gi], s);
     }
-    epilogue_store(ep, y, ydt, n, n, a, cf);
+    if constexpr (EP)
+      epilogue_store(epilogue_after_wait(rg.ep), y, ydt, n, n, a, cf);
+    else if (ydt == BL_I32)
+      static_cast<int32_t*>(y)[n] = a;
+    else if (ydt == BL_F32)
+      static_cast<float*>(y)[n] = __fmul_rn(__int2float_rn(a), cf);
+    else
+      static_cast<__nv_bfloat16*>(y)[n] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
   }
   if (XDT != BL_I8 && write_scale && b == 0 && tid == 0) scale[0] = s;
 }
@@ -467,7 +475,7 @@ __device__ __forceinline__ int dot_seg_t5(const uint4 wv, const uint32_t (&xlo)[
   return v + (vh >> 2);
 }
 
-template <int XDT, int XC, int S, bool ALIGNED>
+template <int XDT, int XC, int S, bool ALIGNED, bool EP>
 __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
     gemv1_t5_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                     int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
@@ -711,7 +719,6 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
 
   // 6. dequantize and store the CTA's outputs (coalesced)
   const float cf1 = dequant_factor(sh_gam[0], s);
-  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = tid; r < nrows; r += T) {
     const int a = rsum[r];
     const int64_t n = row0 + r;
@@ -721,7 +728,14 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
       while (gi + 1 < rg.n && n >= sh_end[gi]) ++gi;
       cf = dequant_factor(sh_gam[gi], s);
     }
-    epilogue_store(ep, y, ydt, n, n, a, cf);
+    if constexpr (EP)
+      epilogue_store(epilogue_after_wait(rg.ep), y, ydt, n, n, a, cf);
+    else if (ydt == BL_I32)
+      static_cast<int32_t*>(y)[n] = a;
+    else if (ydt == BL_F32)
+      static_cast<float*>(y)[n] = __fmul_rn(__int2float_rn(a), cf);
+    else
+      static_cast<__nv_bfloat16*>(y)[n] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
   }
   if (XDT != BL_I8 && write_scale && b == 0 && tid == 0) scale[0] = s;
 }
@@ -761,7 +775,7 @@ __device__ __forceinline__ int dot_seg_b1(const uint4 wv, const uint32_t (&X)[4]
   return a0 + 2 * (a_even + (a_odd >> 1));
 }
 
-template <int XDT, int XC, int S, bool ALIGNED>
+template <int XDT, int XC, int S, bool ALIGNED, bool EP>
 __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
     gemv1_b1_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                     int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
@@ -986,7 +1000,6 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
 
   // 6. dequantize and store the CTA's outputs (coalesced)
   const float cf1 = dequant_factor(sh_gam[0], s);
-  const Epilogue ep = epilogue_after_wait(rg.ep);
   for (int r = tid; r < nrows; r += T) {
     const int a = rsum[r];
     const int64_t n = row0 + r;
@@ -996,7 +1009,14 @@ __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
       while (gi + 1 < rg.n && n >= sh_end[gi]) ++gi;
       cf = dequant_factor(sh_gam[gi], s);
     }
-    epilogue_store(ep, y, ydt, n, n, a, cf);
+    if constexpr (EP)
+      epilogue_store(epilogue_after_wait(rg.ep), y, ydt, n, n, a, cf);
+    else if (ydt == BL_I32)
+      static_cast<int32_t*>(y)[n] = a;
+    else if (ydt == BL_F32)
+      static_cast<float*>(y)[n] = __fmul_rn(__int2float_rn(a), cf);
+    else
+      static_cast<__nv_bfloat16*>(y)[n] = __float2bfloat16_rn(__fmul_rn(__int2float_rn(a), cf));
   }
   if (XDT != BL_I8 && write_scale && b == 0 && tid == 0) scale[0] = s;
 }
@@ -1068,15 +1088,16 @@ static cudaError_t launch_gemv1_t(const Gemv1Geom& g, const uint8_t* packed, int
                                   int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
                                   int write_scale, const RowGroups& rg, void* ws, cudaStream_t st) {
   const bool al = g.lpr % 32 == 0;
-  auto pick = [al]() {
+  auto pick = [al](auto ep) {  // with an epilogue or without: the plain kernels keep their registers
+    constexpr bool EP = decltype(ep)::value;
     if constexpr (FMT == BL_PACK_T5)
-      return al ? gemv1_t5_kernel<XDT, XC, S, true> : gemv1_t5_kernel<XDT, XC, S, false>;
+      return al ? gemv1_t5_kernel<XDT, XC, S, true, EP> : gemv1_t5_kernel<XDT, XC, S, false, EP>;
     else if constexpr (FMT == BL_PACK_B1)
-      return al ? gemv1_b1_kernel<XDT, XC, S, true> : gemv1_b1_kernel<XDT, XC, S, false>;
+      return al ? gemv1_b1_kernel<XDT, XC, S, true, EP> : gemv1_b1_kernel<XDT, XC, S, false, EP>;
     else
-      return al ? gemv1_i2_kernel<XDT, XC, S, true> : gemv1_i2_kernel<XDT, XC, S, false>;
+      return al ? gemv1_i2_kernel<XDT, XC, S, true, EP> : gemv1_i2_kernel<XDT, XC, S, false, EP>;
   };
-  auto kern = pick();
+  auto kern = rg.ep.act >= 0 ? pick(std::true_type{}) : pick(std::false_type{});
   const size_t smem = static_cast<size_t>(g.smem);
   if (smem > 48 * 1024) {
     const cudaError_t e =

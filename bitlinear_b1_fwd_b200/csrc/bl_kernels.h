@@ -69,6 +69,7 @@ cudaError_t launch_ln_quant(const void* x, int xdt, const float* g, const float*
 cudaError_t launch_act_quant(const void* x, int xdt, int64_t M, int64_t K, int8_t* xq, float* scale,
                              cudaStream_t st);
 int gemv_max_tokens(int fmt, int64_t rowbytes);
+bool gemv_epilogue_fits(int64_t M, int64_t N, int64_t rowbytes);
 // tcgen05 GEMM on 2-bit weights; limit_cycles <= 0 uses the default wait limit.
 int gemm_token_tile(int64_t M);
 // y: row t of the output at y + t ldy (ldy >= N).  part: ks x M x N INT32
