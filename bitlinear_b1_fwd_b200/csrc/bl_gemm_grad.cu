@@ -124,9 +124,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int steps = (R + kBR - 1) / kBR;
-  const int j_tiles = (J + 2 * kTile - 1) / (2 * kTile);
-  const int i_tiles = (I + 2 * kTile - 1) / (2 * kTile);
+  const int steps = (R - 1) / kBR + 1;  // I and R reach 2^31 - 1: nothing is added to them
+  const int j_tiles = (J - 1) / (2 * kTile) + 1;
+  const int i_tiles = (I - 1) / (2 * kTile) + 1;
   const int units = i_tiles * j_tiles * ks;  // ks <= steps (host): no unit is empty
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   struct Unit {

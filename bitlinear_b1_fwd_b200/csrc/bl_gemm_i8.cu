@@ -120,8 +120,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int kblocks = (K + kBK - 1) / kBK;
-  const int j_tiles = (N + 2 * kTile - 1) / (2 * kTile);
-  const int tiles = j_tiles * ((M + 2 * kTile - 1) / (2 * kTile)) * ks;  // ks <= kblocks: no part is empty
+  const int j_tiles = (N - 1) / (2 * kTile) + 1;  // M and N reach 2^31 - 1: nothing is added to them
+  const int tiles = j_tiles * ((M - 1) / (2 * kTile) + 1) * ks;  // ks <= kblocks: no part is empty
   // tile u: weight rows u % j_tiles, then part of the contraction, then tokens
   auto tokens_of = [&](int u) { return u / j_tiles / ks * 2 * kTile + static_cast<int>(rank) * kTile; };
   auto part_of = [&](int u) { return u / j_tiles % ks; };
