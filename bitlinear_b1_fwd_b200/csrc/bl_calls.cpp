@@ -135,17 +135,25 @@ void* stream_of(PyObject* o, const Call& call) {
   return p;
 }
 
+// The interpreter is free while one lives, and taken back when an exception
+// (of a device that cannot be made current) leaves its scope too.
+struct Free {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Free() { PyEval_RestoreThread(state); }
+};
+
 // f() with the call's device current and the interpreter free; the caller's
 // device comes back.
 template <typename F>
 PyObject* on_device(const Call& call, F f) {
   int status;
-  Py_BEGIN_ALLOW_THREADS;
-  const auto d = static_cast<c10::DeviceIndex>(call.dev), before = c10::cuda::current_device();
-  if (d != before) c10::cuda::set_device(d);
-  status = f();
-  if (d != before) c10::cuda::set_device(before);
-  Py_END_ALLOW_THREADS;
+  {
+    const Free interpreter;
+    const auto d = static_cast<c10::DeviceIndex>(call.dev), before = c10::cuda::current_device();
+    if (d != before) c10::cuda::set_device(d);
+    status = f();
+    if (d != before) c10::cuda::set_device(before);
+  }
   return PyLong_FromLong(status);
 }
 
