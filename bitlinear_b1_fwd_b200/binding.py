@@ -373,6 +373,9 @@ def bitlinear_residual_norm_backward(dy, dh, b, h, dr, db, ws, post=BL_NORM_NONE
                                                           dpost_w, dpost_b, dgate, dpre_w, dpre_b, stream)
     if status:
         raise BitLinearError(status, "bitlinear_residual_norm_backward")
+    if dgate is not None and dy.shape[0] == 0:  # the C call sees no rows of a gate of no tokens; one shared row has K
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dgate.device)):
+            dgate.zero_()
 
 
 def bitlinear_device_status(ws, stream=None) -> int:

@@ -394,3 +394,12 @@ def test_empty_batch():
     B.bitlinear_residual_norm(e, e, e.clone())
     B.bitlinear_residual_norm_backward(e, None, e, e, e.clone(), e.clone(), ws, dpre_w=w)
     assert (w == 0).all()
+
+
+def test_empty_batch_shared_gate():
+    """No token: the gradient of a gate row shared by all tokens is zero, not what the buffer held."""
+    e, gate = torch.empty(0, 48, device="cuda"), torch.ones(48, device="cuda")
+    ws = torch.zeros(B.bitlinear_residual_norm_backward_workspace_bytes(0, 48), dtype=torch.uint8, device="cuda")
+    dgate = torch.full((48,), 3.0, device="cuda")
+    B.bitlinear_residual_norm_backward(e, None, e, e, e.clone(), e.clone(), ws, gate=gate, dgate=dgate)
+    assert (dgate == 0).all()
