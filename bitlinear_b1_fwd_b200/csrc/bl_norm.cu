@@ -287,9 +287,15 @@ __global__ void __launch_bounds__(norm_max_threads(VEC, NI), VEC * NI <= 8 ? 2 :
     for (int i = 0; i < NI; ++i) {
       const int k = col0<VEC>(i);
       if (kHold || k < W) {
-        Vals<VEC> t = mul(rr[i], splat<VEC>(p.res_scale));
-        if constexpr (BIAS) t = add(t, kHold ? slots.get(2, i) : branch_offset<VEC>(p, gate, k));
-        v[i] = fma(kHold ? slots.get(0, i) : branch_factor<VEC>(p, gate, k), v[i], t);
+        // both products rounded before their sum: it is 0 where they cancel, and the same
+        // with b and r exchanged (one fused product would leave its rounding behind)
+        const Vals<VEC> gw = kHold ? slots.get(0, i) : branch_factor<VEC>(p, gate, k);
+        Vals<VEC> t;
+        if constexpr (BIAS)
+          t = fma(gw, v[i], kHold ? slots.get(2, i) : branch_offset<VEC>(p, gate, k));
+        else
+          t = mul(gw, v[i]);
+        v[i] = add_apart(mul(rr[i], splat<VEC>(p.res_scale)), t);
         if (h != nullptr && k < W) store_vals<RDT, VEC>(ph, k, v[i]);
       }
     }
@@ -358,7 +364,8 @@ __global__ void __launch_bounds__(kNormLongThreads)
       load_col<1>(p.post_w, k, 1.0f, &w);
       load_col<1>(p.post_b, k, 0.0f, &c);
       load_col<1>(gate, k, 1.0f, &g);
-      return p.res_scale * load_elem<RDT>(r, m * K + k) + p.branch_scale * g * ((bv(k) - mean1) * r1 * w + c);
+      const float u = (bv(k) - mean1) * r1 * w + c;  // (two rounded products, as in the other kernel)
+      return __fadd_rn(__fmul_rn(p.res_scale, load_elem<RDT>(r, m * K + k)), __fmul_rn(p.branch_scale * g, u));
     };
     auto yv = [&](float hk, int64_t k) {
       float w, c;

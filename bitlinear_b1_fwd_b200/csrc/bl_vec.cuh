@@ -117,8 +117,9 @@ __device__ __forceinline__ void store_vec_dt(void* p, int dt, int64_t e, const f
 }
 
 // ---- packed fp32 pairs ----------------------------------------------------------
-// add, mul and fma on two fp32 values in one instruction, each value rounded as
-// the scalar instruction rounds it.
+// add, mul and fma on two fp32 values in one instruction.  The assembler makes one
+// fma of a mul and an add that takes its result, which it does not do to the scalar
+// __fmul_rn and __fadd_rn: where a product has to be rounded before a sum, add_apart.
 struct F2 {
   uint64_t v;
   __device__ __forceinline__ F2() {}
@@ -192,6 +193,18 @@ __device__ __forceinline__ Vals<VEC> add(const Vals<VEC>& a, const Vals<VEC>& b)
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) r.p[i] = add(a.p[i], b.p[i]);
   }
+  return r;
+}
+// a + b of values as they were rounded (scalar adds)
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> add_apart(const Vals<VEC>& a, const Vals<VEC>& b) {
+  float x[VEC], y[VEC];
+  a.get(x);
+  b.get(y);
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) x[j] = __fadd_rn(x[j], y[j]);
+  Vals<VEC> r;
+  r.set(x);
   return r;
 }
 template <int VEC>

@@ -374,7 +374,9 @@ BL_API bl_status bitlinear_backward_dw_bf16(const void *dz, const int8_t *xq, co
  * RMS: v / sqrt(mean v^2 + eps);  LAYER: (v - mean v) / sqrt(var v + eps) with
  * the biased variance;  NONE: v.  Everything is computed in fp32 (sums in a
  * fixed order) and rounded once where it is stored; norm_pre sees the
- * unrounded h.  Feeds bitlinear_forward with xdt = BL_I8, or with y. */
+ * unrounded h, the fp32 sum of the two rounded products res_scale r and
+ * branch_scale gate u (0 where they cancel).  Feeds bitlinear_forward with
+ * xdt = BL_I8, or with y. */
 typedef enum { BL_NORM_NONE = 0, BL_NORM_RMS = 1, BL_NORM_LAYER = 2 } bl_norm;
 typedef struct {
   int post;             /* bl_norm of the block's output */
