@@ -351,7 +351,8 @@ def bitlinear_residual_norm(b, r, h, post=BL_NORM_NONE, post_w=None, post_b=None
                             pre_eps=1e-5, y=None, xq=None, scale=None, stream=None) -> None:
     """h = res_scale r + branch_scale gate norm_post(b); y = norm_pre(h); xq, scale its INT8 codes.
 
-    gate: [rows, K] with one row for every gate_rows tokens (0: one row for all, also as [K])."""
+    gate: [rows, K] with one row for every gate_rows tokens (0: one row for all, also as [K]).  Without tokens a shared
+    gate keeps its row, one with rows of its own has one or none."""
     status = (_native or _calls()).residual_norm(b, r, h, post, post_w, post_b, post_eps, gate, gate_rows, res_scale,
                                                  branch_scale, pre, pre_w, pre_b, pre_eps, y, xq, scale, stream)
     if status:
@@ -373,9 +374,6 @@ def bitlinear_residual_norm_backward(dy, dh, b, h, dr, db, ws, post=BL_NORM_NONE
                                                           dpost_w, dpost_b, dgate, dpre_w, dpre_b, stream)
     if status:
         raise BitLinearError(status, "bitlinear_residual_norm_backward")
-    if dgate is not None and dy.shape[0] == 0:  # the C call sees no rows of a gate of no tokens; one shared row has K
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dgate.device)):
-            dgate.zero_()
 
 
 def bitlinear_device_status(ws, stream=None) -> int:

@@ -654,7 +654,7 @@ bl_status bitlinear_residual_norm_backward(const bl_residual_norm_params* p, con
     return BL_ERR_MISALIGNED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M == 0) {
-    float* const sums[4] = {g->dpost_w, g->dpost_b, g->dpre_w, g->dpre_b};  // a gate of no tokens has no rows
+    float* const sums[5] = {g->dpost_w, g->dpost_b, g->dgate, g->dpre_w, g->dpre_b};  // (one gate row)
     for (float* s : sums)
       if (s != nullptr && cudaMemsetAsync(s, 0, K * sizeof(float), st) != cudaSuccess) return BL_ERR_CUDA;
     return BL_OK;

@@ -265,8 +265,13 @@ bl_residual_norm_params norm_params(PyObject* const* a, PyObject* pre_b, PyObjec
   if (a[4] != Py_None) {
     const at::Tensor& gate = tensor("gate", a[4]);
     p.gate_rows = integer(a[5]);
-    if (p.gate_rows < 1) p.gate_rows = M > 1 ? M : 1;  // one row for every token
-    const int64_t rows = M == 0 ? 0 : (M - 1) / p.gate_rows + 1;
+    const bool shared = p.gate_rows < 1;
+    if (shared) p.gate_rows = M > 1 ? M : 1;  // one row for every token
+    // a batch without tokens uses no row: a shared gate has its one all the same,
+    // one with a row for every gate_rows tokens may have none
+    const int64_t rows = M > 0 ? (M - 1) / p.gate_rows + 1
+                         : shared || gate.dim() != 2 || gate.size(0) != 0 ? 1
+                                                                          : 0;
     if (gate.dim() == 1) {
       p.gate = static_cast<const float*>(want("gate", gate, {K}, kF32, call));
       if (rows > 1) refuse(PyExc_ValueError, "gate: one row, expected " + std::to_string(rows));
@@ -326,6 +331,7 @@ PyObject* residual_norm_backward(PyObject* const* a) {
     const at::Tensor& gate = THPVariable_Unpack(a[11]);
     g.dgate = gate.dim() == 1 ? want<float>("dgate", a[20], {K}, kF32, call)
                               : want<float>("dgate", a[20], {gate.size(0), K}, kF32, call);
+    if (gate.numel() == 0) g.dgate = nullptr;  // no row
   }
   const Workspace ws = workspace(a[6], call);
   void* st = stream_of(a[23], call);

@@ -383,7 +383,7 @@ typedef struct {
   float post_eps;       /* > 0 and finite unless post is BL_NORM_NONE */
   const float *post_w;  /* [K], or NULL (1) */
   const float *post_b;  /* [K], or NULL (0) */
-  const float *gate;    /* [ceil(M / gate_rows), K], or NULL (1) */
+  const float *gate;    /* [ceil(M / gate_rows), K] ([1, K] when M is 0), or NULL (1) */
   int64_t gate_rows;    /* token m uses gate row m / gate_rows (>= M: one shared row); >= 1 with a gate */
   float res_scale;      /* finite */
   float branch_scale;   /* finite */
@@ -407,7 +407,8 @@ BL_API bl_status bitlinear_residual_norm(const bl_residual_norm_params *p, const
  *        be dy when the types agree), or NULL;
  *   dpost_w, dpost_b, dpre_w, dpre_b [K] fp32, dgate like gate, each or NULL
  *        (the sums over tokens in fp32, in a fixed order: the same bits on
- *        every call; zeros when M is 0).  dgate needs a gate.
+ *        every call; zeros when M is 0, dgate's one row too).  dgate needs a
+ *        gate.
  *   ws   at least bitlinear_residual_norm_backward_workspace_bytes(M, K,
  *        gate_rows) (gate_rows 0: no gate). */
 typedef struct {
