@@ -837,8 +837,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // bytes 16t .. 16t + 15 of row n (weights 80t .. 80t + 79; bytes past rb5 read
 // as padding, 121 = five weight-0 digits) become 160 bits, i.e. five 32-bit
 // words at byte 20t of the 2-bit row (words past rb2 are dropped).
-// No table: the 32 KB one per block that this replaces
-// took longer to fill than a 3200 x 8640 matrix takes to transcode.
+// No table: the 32 KB one per block that this replaces took longer to fill than
+// a 3200 x 8640 matrix takes to transcode, and 11 us more on 28672 x 8192 (16
+// tokens, with the product: 109 us against 98).
 __global__ void __launch_bounds__(256)
     t5_to_i2_kernel(const uint8_t* __restrict__ t5, int64_t N, int64_t K, int64_t rb5, uint8_t* __restrict__ i2,
                     int64_t rb2) {

@@ -180,31 +180,34 @@ __device__ __forceinline__ uint4 expand16_bits(uint32_t h) {
 // A base-3 segment (16 bytes, 80 weights) as five words of 2-bit codes (a base-3
 // digit is the 2-bit code of the same weight).  With q_i = floor(b / 3^i) the
 // digits of a byte b are d_i = q_i - 3 q_{i+1}, so its ten bits are sum d_i 4^i =
-// b + q_1 + 4 q_2 + 16 q_3 + 64 q_4: four divisions by 3 (the multiply by 171 /
-// 512, exact below 256), two bytes at a time in the 16-bit halves of a register.
+// b + q_1 + 4 q_2 + 16 q_3 + 64 q_4.  floor(x / 3) = floor(85 (x + 1) / 256) for x
+// <= 255 (85 / 256 is 1/3 - 1/768: x = 3 k gives k + 1/3 - (3 k + 1) / 768 >= k, x =
+// 3 k + 2 less than k + 1), two bytes at a time in the 16-bit halves of a register:
+// a multiply-add, and one byte permute that takes the quotients from the halves'
+// upper bytes.  The integer ALU bounds its caller's kernel on large matrices (28672
+// x 8192), so shifts and masks are left to permutes and multiply-adds.
 __device__ __forceinline__ uint32_t t5_pair(uint32_t x) {  // two bytes at bits 0 and 16 -> two 10-bit fields there
-  const uint32_t over = ((x + 0x000d000du) >> 8 & 0x00010001u) * 0xffu;  // bytes 243..255: five weight-0 digits (121)
+  const uint32_t over = __byte_perm(x + 0x000d000du, 0u, 0x4341) * 0xffu;  // bytes 243..255: five weight-0 digits (121)
   x = (x & ~over) | (0x00790079u & over);
-  const uint32_t q1 = (x * 171u >> 9) & 0x007f007fu;
-  const uint32_t q2 = (q1 * 171u >> 9) & 0x007f007fu;
-  const uint32_t q3 = (q2 * 171u >> 9) & 0x007f007fu;
-  const uint32_t q4 = (q3 * 171u >> 9) & 0x007f007fu;
+  auto third = [](uint32_t v) { return __byte_perm(v * 85u + 0x00550055u, 0u, 0x4341); };
+  const uint32_t q1 = third(x), q2 = third(q1), q3 = third(q2), q4 = third(q3);
   return x + q1 + 4u * q2 + 16u * q3 + 64u * q4;
 }
 __device__ __forceinline__ void t5_segment(const uint4& v, uint32_t* out) {
   const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-  uint64_t f[4];  // 40 bits of each packed word
+  uint32_t lo[4], hi[4];  // 40 bits of each packed word: 32 and 8
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t a = t5_pair(wd[i] & 0x00ff00ffu), c = t5_pair((wd[i] >> 8) & 0x00ff00ffu);  // bytes 0, 2 and 1, 3
-    const uint32_t lo = (a & 0x3ffu) | (c & 0x3ffu) << 10, hi = a >> 16 | (c >> 16) << 10;
-    f[i] = static_cast<uint64_t>(lo) | static_cast<uint64_t>(hi) << 20;
+    // bytes 0, 2 and 1, 3: the upper field moves from bit 16 to bit 20
+    const uint32_t a = t5_pair(__byte_perm(wd[i], 0u, 0x4240)), c = t5_pair(__byte_perm(wd[i], 0u, 0x4341));
+    lo[i] = a + (a >> 16) * 0xf0000u + (c + (c >> 16) * 0xf0000u) * 1024u;
+    hi[i] = c >> 18;
   }
-  out[0] = static_cast<uint32_t>(f[0]);
-  out[1] = static_cast<uint32_t>(f[0] >> 32) | static_cast<uint32_t>(f[1]) << 8;
-  out[2] = static_cast<uint32_t>(f[1] >> 24) | static_cast<uint32_t>(f[2]) << 16;
-  out[3] = static_cast<uint32_t>(f[2] >> 16) | static_cast<uint32_t>(f[3]) << 24;
-  out[4] = static_cast<uint32_t>(f[3] >> 8);
+  out[0] = lo[0];
+  out[1] = __byte_perm(hi[0], lo[1], 0x6540);
+  out[2] = __byte_perm(__byte_perm(lo[1], hi[1], 0x0043), lo[2], 0x5410);
+  out[3] = __byte_perm(__byte_perm(lo[2], hi[2], 0x0432), lo[3], 0x4210);
+  out[4] = __byte_perm(lo[3], hi[3], 0x4321);
 }
 
 // ---- bulk copies (no tensor map) and bulk-group waits --------------------------------
