@@ -393,7 +393,7 @@ bl_status bitlinear_forward_grouped(const uint8_t* packed, int fmt, const float*
       fmt = BL_PACK_I2;
     }
     if (bl::gemv_max_tokens(fmt, bitlinear_packed_row_bytes(K, fmt)) < 1) return BL_ERR_UNSUPPORTED;
-    bl::RowGroups rg{};
+    bl::RowGroupsEp rg{};
     rg.n = static_cast<int>(ngroups);
     rg.ep = bl::no_epilogue();
     int64_t end = 0;

@@ -890,7 +890,7 @@ template <int MT, int XDT, bool EP>
 __global__ void __launch_bounds__(kMtThreads, 1)
     gemv_i2_mt_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                       int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
-                      void* __restrict__ y, int ydt, int write_scale, const RowGroups rg) {
+                      void* __restrict__ y, int ydt, int write_scale, const KernelGroups<EP> rg) {
   const int64_t G = gridDim.x, b = blockIdx.x;
   const int64_t per = N / G, extra = N % G;
   const int64_t row0 = b * per + (b < extra ? b : extra);
@@ -1346,7 +1346,7 @@ int gemv_max_tokens(int fmt, int64_t rowbytes) {
 template <int FMT, int MT, int XDT>
 static cudaError_t launch_gemv_t(const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                  int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                 int write_scale, const RowGroups& rg, cudaStream_t st) {
+                                 int write_scale, const RowGroupsEp& rg, cudaStream_t st) {
   auto kern = gemv_kernel<FMT, MT, XDT>;
   const size_t smem = static_cast<size_t>(gemv_smem_bytes(FMT, rowbytes, MT));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1369,7 +1369,7 @@ static cudaError_t launch_gemv_t(const uint8_t* packed, int64_t rowbytes, const 
 template <int FMT, int MT, int XDT>
 static cudaError_t launch_gemv_i2_t(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N,
                                     int64_t K, const void* x, float* scale, void* y, int ydt, int write_scale,
-                                    const RowGroups& rg, cudaStream_t st) {
+                                    const RowGroupsEp& rg, cudaStream_t st) {
   auto kern = gemv_i2_kernel<FMT, MT, XDT>;
   const size_t smem = static_cast<size_t>(gemv_i2_smem_bytes(MT));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1384,7 +1384,7 @@ static cudaError_t launch_gemv_i2_t(const uint8_t* packed, int64_t rowbytes, con
 template <int FMT, int XDT>
 static cudaError_t launch_gemv_i2_mt(int mt, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                      int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                     int write_scale, const RowGroups& rg, cudaStream_t st) {
+                                     int write_scale, const RowGroupsEp& rg, cudaStream_t st) {
   switch (mt) {
     case 1: return launch_gemv_i2_t<FMT, 1, XDT>(packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
     case 2: return launch_gemv_i2_t<FMT, 2, XDT>(packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
@@ -1396,7 +1396,7 @@ static cudaError_t launch_gemv_i2_mt(int mt, const uint8_t* packed, int64_t rowb
 template <int XDT>
 static cudaError_t launch_gemv_lean(int fmt, int mt, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                     int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                    int write_scale, const RowGroups& rg, cudaStream_t st) {
+                                    int write_scale, const RowGroupsEp& rg, cudaStream_t st) {
   if (fmt == BL_PACK_B1)
     return launch_gemv_i2_mt<BL_PACK_B1, XDT>(mt, packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
   return launch_gemv_i2_mt<BL_PACK_I2, XDT>(mt, packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
@@ -1414,15 +1414,18 @@ static bool gemv_mt_fits(int64_t rowbytes, int64_t N, int mt) {
 template <int MT, int XDT>
 static cudaError_t launch_gemv_mt_cs(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N,
                                      int64_t K, const void* x, float* scale, void* y, int ydt, int write_scale,
-                                     const RowGroups& rg, cudaStream_t st) {
-  auto kern = rg.ep.act >= 0 ? gemv_i2_mt_kernel<MT, XDT, true> : gemv_i2_mt_kernel<MT, XDT, false>;
-  const size_t smem = static_cast<size_t>(gemv_mt_smem_bytes(rowbytes, MT));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  const int64_t sms = device_sms();
-  const int64_t grid = N < sms ? N : sms;  // every CTA owns at least one row
-  e = launch_pdl(kern, static_cast<unsigned>(grid), kMtThreads, smem, st, packed, rowbytes, gamma, N, K, x, scale, y,
-                 ydt, write_scale, rg);
+                                     const RowGroupsEp& rg, cudaStream_t st) {
+  auto run = [&](auto kern) {
+    const size_t smem = static_cast<size_t>(gemv_mt_smem_bytes(rowbytes, MT));
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t sms = device_sms();
+    const int64_t grid = N < sms ? N : sms;  // every CTA owns at least one row
+    return launch_pdl(kern, static_cast<unsigned>(grid), kMtThreads, smem, st, packed, rowbytes, gamma, N, K, x, scale,
+                      y, ydt, write_scale, rg);
+  };
+  const cudaError_t e = rg.ep.act >= 0 ? run(gemv_i2_mt_kernel<MT, XDT, true>) : run(gemv_i2_mt_kernel<MT, XDT, false>);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1430,7 +1433,7 @@ static cudaError_t launch_gemv_mt_cs(const uint8_t* packed, int64_t rowbytes, co
 template <int XDT>
 static cudaError_t launch_gemv_mt_cs_n(int mt, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                        int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                       int write_scale, const RowGroups& rg, cudaStream_t st) {
+                                       int write_scale, const RowGroupsEp& rg, cudaStream_t st) {
   switch (mt) {
     case 2: return launch_gemv_mt_cs<2, XDT>(packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
     case 3: return launch_gemv_mt_cs<3, XDT>(packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
@@ -1450,7 +1453,7 @@ static bool gemv_t5_fits(int64_t rowbytes, int64_t N) {
 template <int XDT>
 static cudaError_t launch_gemv_t5_t(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N,
                                     int64_t K, const void* x, float* scale, void* y, int ydt, int write_scale,
-                                    const RowGroups& rg, cudaStream_t st) {
+                                    const RowGroupsEp& rg, cudaStream_t st) {
   auto kern = gemv_t5_kernel<XDT>;
   const size_t smem = static_cast<size_t>(gemv_t5_smem_bytes(rowbytes));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1466,7 +1469,7 @@ static cudaError_t launch_gemv_t5_t(const uint8_t* packed, int64_t rowbytes, con
 template <int FMT, int XDT>
 static cudaError_t launch_gemv_mt(int mt, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                   int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                  int write_scale, const RowGroups& rg, cudaStream_t st) {
+                                  int write_scale, const RowGroupsEp& rg, cudaStream_t st) {
   switch (mt) {
     case 1: return launch_gemv_t<FMT, 1, XDT>(packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
     case 2: return launch_gemv_t<FMT, 2, XDT>(packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, st);
@@ -1483,7 +1486,7 @@ bool gemv_epilogue_fits(int64_t M, int64_t N, int64_t rowbytes) {
 // Runs the GEMV over all M tokens in groups that fit in shared memory.
 cudaError_t launch_gemv(const uint8_t* packed, int fmt, const float* gamma, int64_t N, int64_t K,
                         const void* x, int xdt, float* scale, int64_t M, void* y, int ydt,
-                        const RowGroups& rg, void* ws, cudaStream_t st) {
+                        const RowGroupsEp& rg, void* ws, cudaStream_t st) {
   const int per = (fmt == BL_PACK_I2) ? 4 : (fmt == BL_PACK_T5 ? 5 : 8);
   const int64_t rowbytes = ((K + per - 1) / per + 15) / 16 * 16;
   const int mt_max = gemv_max_tokens(fmt, rowbytes);

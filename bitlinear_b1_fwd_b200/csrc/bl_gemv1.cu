@@ -167,7 +167,7 @@ template <int XDT, int XC, int S, bool ALIGNED, bool EP>
 __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
     gemv1_i2_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                     int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
-                    void* __restrict__ y, int ydt, int write_scale, const RowGroups rg, int R, int lpr, void* ws) {
+                    void* __restrict__ y, int ydt, int write_scale, const KernelGroups<EP> rg, int R, int lpr, void* ws) {
   constexpr int kXW = g1_xwords<XDT>();
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t red[kG1MaxThreads / 32];
@@ -479,7 +479,7 @@ template <int XDT, int XC, int S, bool ALIGNED, bool EP>
 __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
     gemv1_t5_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                     int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
-                    void* __restrict__ y, int ydt, int write_scale, const RowGroups rg, int R, int lpr, void* ws) {
+                    void* __restrict__ y, int ydt, int write_scale, const KernelGroups<EP> rg, int R, int lpr, void* ws) {
   constexpr int kXW = g1_xwords<XDT>();
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t red[kG1MaxThreads / 32];
@@ -779,7 +779,7 @@ template <int XDT, int XC, int S, bool ALIGNED, bool EP>
 __global__ void __launch_bounds__(kG1MaxThreads, 1024 / kG1MaxThreads)
     gemv1_b1_kernel(const uint8_t* __restrict__ packed, int64_t rowbytes, const float* __restrict__ gamma,
                     int64_t N, int64_t K, const void* __restrict__ x, float* __restrict__ scale,
-                    void* __restrict__ y, int ydt, int write_scale, const RowGroups rg, int R, int lpr, void* ws) {
+                    void* __restrict__ y, int ydt, int write_scale, const KernelGroups<EP> rg, int R, int lpr, void* ws) {
   constexpr int kXW = g1_xwords<XDT>();
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t red[kG1MaxThreads / 32];
@@ -1086,7 +1086,7 @@ bool gemv1_b1_fits(int64_t N, int64_t K, int64_t rowbytes, int xdt) {
 template <int FMT, int XDT, int XC, int S>
 static cudaError_t launch_gemv1_t(const Gemv1Geom& g, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                   int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                  int write_scale, const RowGroups& rg, void* ws, cudaStream_t st) {
+                                  int write_scale, const RowGroupsEp& rg, void* ws, cudaStream_t st) {
   const bool al = g.lpr % 32 == 0;
   auto pick = [al](auto ep) {  // with an epilogue or without: the plain kernels keep their registers
     constexpr bool EP = decltype(ep)::value;
@@ -1097,15 +1097,17 @@ static cudaError_t launch_gemv1_t(const Gemv1Geom& g, const uint8_t* packed, int
     else
       return al ? gemv1_i2_kernel<XDT, XC, S, true, EP> : gemv1_i2_kernel<XDT, XC, S, false, EP>;
   };
-  auto kern = rg.ep.act >= 0 ? pick(std::true_type{}) : pick(std::false_type{});
-  const size_t smem = static_cast<size_t>(g.smem);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  const cudaError_t e = launch_pdl(kern, static_cast<unsigned>(g.grid), static_cast<unsigned>(g.threads), smem, st,
-                                   packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, g.R, g.lpr, ws);
+  auto run = [&](auto kern) {
+    const size_t smem = static_cast<size_t>(g.smem);
+    if (smem > 48 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, static_cast<unsigned>(g.grid), static_cast<unsigned>(g.threads), smem, st, packed, rowbytes,
+                      gamma, N, K, x, scale, y, ydt, write_scale, rg, g.R, g.lpr, ws);
+  };
+  const cudaError_t e = rg.ep.act >= 0 ? run(pick(std::true_type{})) : run(pick(std::false_type{}));
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1113,7 +1115,7 @@ static cudaError_t launch_gemv1_t(const Gemv1Geom& g, const uint8_t* packed, int
 template <int FMT, int XDT, int XC>
 static cudaError_t launch_gemv1_s(const Gemv1Geom& g, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                   int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                  int write_scale, const RowGroups& rg, void* ws, cudaStream_t st) {
+                                  int write_scale, const RowGroupsEp& rg, void* ws, cudaStream_t st) {
   if constexpr (FMT != BL_PACK_B1) {  // the 1-bit kernel runs with 6 stages only
     if (g.stages == kG1StagesMax)
       return launch_gemv1_t<FMT, XDT, XC, kG1StagesMax>(g, packed, rowbytes, gamma, N, K, x, scale, y, ydt,
@@ -1125,7 +1127,7 @@ static cudaError_t launch_gemv1_s(const Gemv1Geom& g, const uint8_t* packed, int
 template <int FMT, int XDT>
 static cudaError_t launch_gemv1_x(const Gemv1Geom& g, const uint8_t* packed, int64_t rowbytes, const float* gamma,
                                   int64_t N, int64_t K, const void* x, float* scale, void* y, int ydt,
-                                  int write_scale, const RowGroups& rg, void* ws, cudaStream_t st) {
+                                  int write_scale, const RowGroupsEp& rg, void* ws, cudaStream_t st) {
   if (g.xc == 1)
     return launch_gemv1_s<FMT, XDT, 1>(g, packed, rowbytes, gamma, N, K, x, scale, y, ydt, write_scale, rg, ws, st);
   if (g.xc == 2)
@@ -1135,7 +1137,7 @@ static cudaError_t launch_gemv1_x(const Gemv1Geom& g, const uint8_t* packed, int
 
 template <int FMT>
 static cudaError_t launch_gemv1_f(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N, int64_t K,
-                                  const void* x, int xdt, float* scale, void* y, int ydt, const RowGroups& rg,
+                                  const void* x, int xdt, float* scale, void* y, int ydt, const RowGroupsEp& rg,
                                   void* ws, cudaStream_t st) {
   Gemv1Geom g;
   if (!gemv1_geom(N, K, rowbytes, xdt, &g, FMT)) return cudaErrorInvalidValue;
@@ -1147,19 +1149,19 @@ static cudaError_t launch_gemv1_f(const uint8_t* packed, int64_t rowbytes, const
 }
 
 cudaError_t launch_gemv1(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N, int64_t K,
-                         const void* x, int xdt, float* scale, void* y, int ydt, const RowGroups& rg, void* ws,
+                         const void* x, int xdt, float* scale, void* y, int ydt, const RowGroupsEp& rg, void* ws,
                          cudaStream_t st) {
   return launch_gemv1_f<BL_PACK_I2>(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
 }
 
 cudaError_t launch_gemv1_t5(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N, int64_t K,
-                            const void* x, int xdt, float* scale, void* y, int ydt, const RowGroups& rg, void* ws,
+                            const void* x, int xdt, float* scale, void* y, int ydt, const RowGroupsEp& rg, void* ws,
                             cudaStream_t st) {
   return launch_gemv1_f<BL_PACK_T5>(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
 }
 
 cudaError_t launch_gemv1_b1(const uint8_t* packed, int64_t rowbytes, const float* gamma, int64_t N, int64_t K,
-                            const void* x, int xdt, float* scale, void* y, int ydt, const RowGroups& rg, void* ws,
+                            const void* x, int xdt, float* scale, void* y, int ydt, const RowGroupsEp& rg, void* ws,
                             cudaStream_t st) {
   return launch_gemv1_f<BL_PACK_B1>(packed, rowbytes, gamma, N, K, x, xdt, scale, y, ydt, rg, ws, st);
 }
