@@ -291,9 +291,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       if (!ok) break;
       const int i0 = w.it * 2 * kTile + static_cast<int>(rank) * kTile + 32 * q, i = i0 + lane;
       const int j0 = w.jt * 2 * kTile + half * kTile;
-      const float alpha = ks > 1 ? 1.0f
-                          : DW   ? (i < I ? __fmul_rn(g, __ldcg(rowinv + i)) : 0.0f)
-                                 : g;
+      float alpha = ks > 1 ? 1.0f : g, inv = 1.0f;
+      if constexpr (DW) {
+        inv = i < I ? __ldcg(rowinv + i) : 0.0f;
+        // a power of two: one factor for both, unless that has no 24 bits (a row of gradients below some 2^-100)
+        if (const float both = __fmul_rn(g, inv); fabsf(both) >= 1.17549435e-38f) {
+          alpha = both;
+          inv = 1.0f;
+        }
+      }
+      auto scaled = [&](float v) { return DW ? __fmul_rn(__fmul_rn(v, alpha), inv) : __fmul_rn(v, alpha); };
       // 32 rows x 128 bytes at a time through this warp's boxes; the TMA unit clips
       // rows past I and columns past J.  (Two boxes of 64-byte rows: 130 tokens,
       // 3200 x 3200, 53 us for both products against 45.)  Rows of the output that
@@ -339,8 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
           next_box(j / 32);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            put(c, __float_as_uint(__fmul_rn(sum[j + 4 * c], alpha)), __float_as_uint(__fmul_rn(sum[j + 4 * c + 1], alpha)),
-                __float_as_uint(__fmul_rn(sum[j + 4 * c + 2], alpha)), __float_as_uint(__fmul_rn(sum[j + 4 * c + 3], alpha)));
+            put(c, __float_as_uint(scaled(sum[j + 4 * c])), __float_as_uint(scaled(sum[j + 4 * c + 1])),
+                __float_as_uint(scaled(sum[j + 4 * c + 2])), __float_as_uint(scaled(sum[j + 4 * c + 3])));
           store(j);
         }
       } else {
@@ -350,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float* v = sum + j + 8 * c;
-            auto two = [&](int k) { return bf16_pair(__fmul_rn(v[k], alpha), __fmul_rn(v[k + 1], alpha)); };
+            auto two = [&](int k) { return bf16_pair(scaled(v[k]), scaled(v[k + 1])); };
             put(c, two(0), two(2), two(4), two(6));
           }
           store(j);
