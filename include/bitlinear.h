@@ -350,7 +350,10 @@ BL_API bl_status bitlinear_epilogue_backward(const void *dy, int dydt, const voi
  * Both add runs of contracted elements (512 for dx, 256 for dW) on the tensor
  * core in fp32 and the runs in fp32 registers in order: the same bits on every
  * call (dx of up to 32 tokens: runs of the same length on another kernel).  The
- * error is below 2^-16 sum |terms| (at most 32 truncating additions a run).
+ * error is below (2^-17 + (17 + R) 2^-24) sum |terms| for R runs (R = N / 512 for
+ * dx, M / 256 for dW): at most 32 truncating additions in a run, each below 2^-22
+ * of it, and a rounded one for each run and each part of a cut contraction.  That
+ * is 2^-16 for 56832 rows (dx) or 28416 tokens (dW), and grows with longer ones.
  *   packed, fmt, gamma  as for bitlinear_forward.
  *   dx   [M, K] BL_F32 or BL_BF16;  dw [N, K] fp32 (zeros when M is 0).
  *   xq, scale           the forward's codes and scales.
