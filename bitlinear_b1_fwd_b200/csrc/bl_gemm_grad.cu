@@ -12,7 +12,8 @@
 // For dW the token's factor varies along the contraction and cannot move to
 // the epilogue: v = fl(dz s_m) is scaled by a power of two per output row n
 // (the row's largest |v| near 2^13) and split into two fp16 parts, hi = fp16(v)
-// and lo = fp16(v - hi): 22 bits of v, against x_q exact in fp16.  Two bf16
+// and lo = fp16(v - hi): 22 bits of v, or 2^-25 (the subnormals' half step, 2^-38 of
+// the row's largest) where that is more, against x_q exact in fp16.  Two bf16
 // parts would keep 16 bits and cost the same.  The epilogue undoes the scale.
 //
 // A cluster of two CTAs computes a tile of 256 x 256 outputs with

@@ -344,9 +344,12 @@ BL_API bl_status bitlinear_epilogue_backward(const void *dy, int dydt, const voi
  * dx = gamma dz . W_q and dW = gamma dz^T . x_deq as bitlinear_backward_dx /
  * _dw, from a bf16 gradient dz [M, N] and with fp32 sums instead of fp64:
  *   dx: the products are exact (bf16 x {-1, 0, 1});
- *   dW: dz s_m is rounded to fp32 and carried as two fp16 parts (22 bits,
- *       scaled by a power of two per output row n, so that the row's largest
- *       entry is near 2^13), times the exact x_q.
+ *   dW: dz s_m is rounded to fp32 and carried as two fp16 parts, scaled by a
+ *       power of two per output row n so that the row's largest entry v_n is
+ *       at 2^13, times the exact x_q: 22 bits of an entry, but no less than
+ *       2^-38 v_n (an entry far below the row's largest loses bits, and from
+ *       2^-39 v_n on is 0).  A row with an infinity, a NaN or a dz s_m beyond
+ *       fp32 gives a row of NaN.
  * Both add runs of contracted elements (512 for dx, 256 for dW) on the tensor
  * core in fp32 and the runs in fp32 registers in order: the same bits on every
  * call (dx of up to 32 tokens: runs of the same length on another kernel).  The
@@ -354,6 +357,7 @@ BL_API bl_status bitlinear_epilogue_backward(const void *dy, int dydt, const voi
  * dx, M / 256 for dW): at most 32 truncating additions in a run, each below 2^-22
  * of it, and a rounded one for each run and each part of a cut contraction.  That
  * is 2^-16 for 56832 rows (dx) or 28416 tokens (dW), and grows with longer ones.
+ * dW's terms add 2^-38 v_n gamma sum_m |x_q[m, k]| / 127 to it.
  *   packed, fmt, gamma  as for bitlinear_forward.
  *   dx   [M, K] BL_F32 or BL_BF16;  dw [N, K] fp32 (zeros when M is 0).
  *   xq, scale           the forward's codes and scales.
