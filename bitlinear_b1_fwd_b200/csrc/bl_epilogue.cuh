@@ -12,8 +12,9 @@ namespace bl {
 
 // Each activation in two forms.  For outputs of 24 bits, within 8 u |a| (GELU: and
 // a few u z^2 |a|), u = 2^-24.  For bf16 outputs (half a step is 2^-9 to 2^-8 of
-// the value) the hardware's exponential and reciprocal, within 2^-17 |a| while
-// |z| < 100; below -87, where the result is under 2^-119, it goes to 0.  Every
+// the value) the hardware's exponential and reciprocal: SiLU within 2^-17 |a| while
+// |z| < 100, GELU within (4 + z^2 / 2) 2^-22 |a| (its exponent is rounded twice);
+// results under 2^-118 may be 0.  Every
 // kernel uses the same form for the same output type.  The difference is some 15
 // and 40 instructions per output: 4096 x 3200 -> 8640 with SiLU and the kept
 // pre-activation took 123 us with the first form and 109 with the second, with

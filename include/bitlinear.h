@@ -299,8 +299,8 @@ BL_API bl_status bitlinear_backward_dw(const void *dy, int dydt, const int8_t *x
  * kernel that serves the sizes (acc is an exact integer, c_m z two fp32
  * roundings): a token gives the same y alone and in a batch.  SiLU and GELU
  * are within 8 u |act| of the formula for fp32 y (GELU and a few u z^2 |act|; u =
- * 2^-24), and within 2^-17 |act| before the rounding for bf16 y, where results
- * below 2^-119 become 0.
+ * 2^-24).  Before the rounding to bf16 y SiLU is within 2^-17 |act| and GELU
+ * within (4 + z^2 / 2) 2^-22 |act|, and results below 2^-118 may be 0.
  *   packed, fmt, gamma, x, xdt, scale  as for bitlinear_forward.
  *   bias      [N] fp32, or NULL (0).
  *   act       bl_act; BL_ACT_GELU is z Phi(z) with the error function.
@@ -331,7 +331,11 @@ BL_API bl_status bitlinear_forward_epilogue(const uint8_t *packed, int fmt, cons
  *   dbias[n] = sum_m dz[m, n]              (of the unrounded fp32 products,
  *              fp32 sums in a fixed order: the same bits on every call);
  * the residual's gradient is dy itself.  act' is 0 where z = 0 for the two
- * ReLUs; with BL_ACT_NONE z may be NULL.
+ * ReLUs; with BL_ACT_NONE z may be NULL.  As computed it is off by at most
+ *   SiLU  (3 + |z|) 2^-22 s (1 + |z|),           s = 1 / (1 + exp(-z)),
+ *   GELU  (4 + z^2 / 2) 2^-22 (Phi(z) + |z| phi(z)),
+ * and for bf16 dy it may be 0 below 2^-118; dz and the terms of dbias are off by
+ * that times |dy| and half a step of fp32.
  *   dy, dz [M, N] of type dydt (dz may be dy, or NULL);  z [M, N] of type zdt.
  *   dbias  [N] fp32, or NULL (not both NULL); zeros when M is 0.
  *   ws     at least bitlinear_epilogue_backward_workspace_bytes(M, N). */
