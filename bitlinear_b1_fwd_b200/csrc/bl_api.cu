@@ -328,7 +328,7 @@ bl_status bitlinear_forward_epilogue(const uint8_t* packed, int fmt, const float
   if (bl::launch_gemm_operands(packed, fmt, rb, N, K, w8, x, xdt, M, padded_codes(K), codes, scale, st) != cudaSuccess)
     return BL_ERR_CUDA;
   return cuda_status(bl::launch_gemm_i8(xq, padded_codes(K), w8, bl::gemm_i8_row(K, fmt), gamma, scale, y, ydt, M, N, K,
-                                        ep, reinterpret_cast<int32_t*>(scratch), ws, st));
+                                        ep, reinterpret_cast<int32_t*>(scratch), ws, 0, 0, st));
 }
 
 // Several weight matrices sharing one token batch (for example a block's Q, K
@@ -685,13 +685,20 @@ bl_status bitlinear_residual_norm_backward(const bl_residual_norm_params* p, con
 }
 
 bl_status bitlinear_selftest_wait_timeout(void* ws, size_t ws_bytes, void* stream) {
-  // 16 tokens x 128 rows x 128 K: the header plus 8 KB of operand space that is never touched
+  // 16 tokens x 128 rows x 128 K: the header plus 8 KB, whose first floats the kernels may read as gamma and
+  // scales; the operands are never touched
   if (ws == nullptr || ws_bytes < BL_WS_HEADER_BYTES + 8192) return BL_ERR_INVALID_VALUE;
   if (!aligned(ws, 16)) return BL_ERR_MISALIGNED;
   uint8_t* op = static_cast<uint8_t*>(ws) + BL_WS_HEADER_BYTES;
   const float* g = reinterpret_cast<const float*>(op);
-  return cuda_status(bl::launch_gemm_i2(reinterpret_cast<const int8_t*>(op), op, 32, g, g, op, BL_I32, 16, 128,
-                                        128, 128, nullptr, ws, int64_t{1} << 20, 1, static_cast<cudaStream_t>(stream)));
+  const int8_t* x = reinterpret_cast<const int8_t*>(op);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  constexpr long long kLimit = 1ll << 20;
+  cudaError_t e = bl::launch_gemm_i2(x, op, 32, g, g, op, BL_I32, 16, 128, 128, 128, nullptr, ws, kLimit, 1, st);
+  if (e == cudaSuccess)
+    e = bl::launch_gemm_i8(x, 128, x, 128, g, g, op, BL_F32, 16, 64, 128, bl::Epilogue{nullptr, nullptr, nullptr, BL_ACT_NONE},
+                           nullptr, ws, kLimit, 1, st);
+  return cuda_status(e == cudaSuccess ? bl::launch_grad_selftest(op, ws, kLimit, st) : e);
 }
 
 bl_status bitlinear_device_status(void* ws, void* stream) {

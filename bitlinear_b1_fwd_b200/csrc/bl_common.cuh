@@ -16,6 +16,8 @@ constexpr int kLanes = 256;
 // Device flags in the first word of a workspace header.
 constexpr uint32_t kFlagTimeout = 1u;
 constexpr uint32_t kFlagBadCode = 2u;
+// which product's wait ran out, beside kFlagTimeout (neither: the 2-bit GEMM or a decode kernel)
+constexpr uint32_t kFlagProductI8 = 0x100u, kFlagProductGrad = 0x200u;
 
 struct WsHeader {
   uint32_t flags;   // kFlag* bits, sticky until bitlinear_device_status

@@ -106,7 +106,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     gemm_grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a2,
                      const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_o,
                      const float* __restrict__ gamma, const float* __restrict__ rowinv, void* __restrict__ out, int I, int J, int R, int ks,
-                     float* __restrict__ part, WsHeader* __restrict__ hdr, long long limit) {
+                     float* __restrict__ part, WsHeader* __restrict__ hdr, long long limit, int skip_producer) {
   pdl_enter(gamma, rowinv, out, part, hdr);
   using Cfg = GradCfg<DW, SHORT>;
   constexpr int S = Cfg::kStages;
@@ -169,13 +169,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto fail = [&](uint32_t site) {
-    set_flag(hdr, kFlagTimeout, site);
+    set_flag(hdr, kFlagTimeout | kFlagProductGrad, site);
     *abort_flag = 1;
   };
 
   if (warp == 0) {
     // ------------------------------ TMA producer (both CTAs) ------------------
-    if (lane == 0) {
+    if (lane == 0 && !skip_producer) {
       int it = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs) {
@@ -612,7 +612,8 @@ unsigned flat_grid(int64_t items) {
 template <bool DW>
 cudaError_t launch_product(const void* a, const void* a2, int64_t lda, const void* b, int64_t ldb, const float* gamma,
                            const float* rowinv, void* out, int odt, int64_t I, int64_t J, int64_t R, int ks,
-                           float* part, void* ws, cudaStream_t st) {
+                           float* part, void* ws, cudaStream_t st, long long limit = kGradTimeout,
+                           int skip_producer = 0) {
   CUtensorMap ta, ta2, tb, to;
   // A: [I, R] K-major (dx) or [R, I] (dW); B: [R, J]
   const bool ok =
@@ -647,7 +648,7 @@ cudaError_t launch_product(const void* a, const void* a2, int64_t lda, const voi
   const int64_t most = device_sms() / 2, pairs = units < most ? units : most;
   return launch_pdl(kern, static_cast<unsigned>(2 * pairs), kGradThreads, smem, st, ta, ta2, tb, to, gamma, rowinv, out,
                     static_cast<int>(I), static_cast<int>(J), static_cast<int>(R), ks, part,
-                    static_cast<WsHeader*>(ws), kGradTimeout);
+                    static_cast<WsHeader*>(ws), limit, skip_producer);
 }
 
 }  // namespace
@@ -722,6 +723,15 @@ cudaError_t launch_grad_dw(const uint16_t* dz, const int8_t* xq, const float* sc
                    s.rowinv, static_cast<__half*>(s.hi), static_cast<__half*>(s.lo));
   if (e == cudaSuccess)
     e = launch_product<true>(s.hi, s.lo, ldn, s.x, ldk, gamma, s.rowinv, dw, BL_F32, N, K, M, 1, nullptr, ws, st);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_grad_selftest(void* op, void* ws, long long limit, cudaStream_t st) {
+  const float* f = static_cast<const float*>(op);
+  cudaError_t e = launch_product<false>(op, nullptr, 64, op, 64, f, nullptr, op, BL_F32, 16, 64, 16, 1, nullptr, ws, st,
+                                        limit, 1);
+  if (e == cudaSuccess)
+    e = launch_product<true>(op, op, 64, op, 64, f, f, op, BL_F32, 16, 64, 16, 1, nullptr, ws, st, limit, 1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

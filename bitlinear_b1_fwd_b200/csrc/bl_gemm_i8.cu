@@ -100,7 +100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
                    const __grid_constant__ CUtensorMap tm_p, int o_tma, const float* __restrict__ gamma,
                    const float* __restrict__ scale, void* __restrict__ y, int M, int N, int K, int ks,
-                   WsHeader* __restrict__ hdr, long long limit, const Epilogue ep_arg) {
+                   WsHeader* __restrict__ hdr, long long limit, int skip_producer, const Epilogue ep_arg) {
   pdl_enter(gamma, scale, y, hdr);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -154,13 +154,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto fail = [&](uint32_t site) {
-    set_flag(hdr, kFlagTimeout, site);
+    set_flag(hdr, kFlagTimeout | kFlagProductI8, site);
     *abort_flag = 1;
   };
 
   if (warp == 0) {
     // ------------------------------ TMA producer (both CTAs) ------------------
-    if (lane == 0) {
+    if (lane == 0 && !skip_producer) {
       int it = 0;
       bool ok = true;
       for (int u = pair; u < tiles && ok; u += pairs) {
@@ -628,14 +628,14 @@ cudaError_t launch_gemm_operands(const uint8_t* packed, int fmt, int64_t rowbyte
 
 cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64_t ldw, const float* gamma,
                            const float* scale, void* y, int ydt, int64_t M, int64_t N, int64_t K, const Epilogue& ep,
-                           int32_t* part, void* ws, cudaStream_t st) {
+                           int32_t* part, void* ws, long long limit, int skip_producer, cudaStream_t st) {
   CUtensorMap tx, tw, ty, tr, tp;
   if (!encode_2d_u8(&tx, xq, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(ldx), kBK, kTile,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d_u8(&tw, w, static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(ldw), kBK, kTile,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int ks = gemm_i8_parts(M, N, K);
+  const int ks = skip_producer ? 1 : gemm_i8_parts(M, N, K);
   const int odt = ks > 1 ? static_cast<int>(BL_I32) : ydt;
   void* out = ks > 1 ? part : y;
   auto box_map = [&](CUtensorMap* m, const void* p) {
@@ -655,7 +655,7 @@ cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64
   const int64_t most = device_sms() / 2, pairs = tiles < most ? tiles : most;
   e = launch_pdl(kern, static_cast<unsigned>(2 * pairs), kThreads, kSmem, st, tx, tw, ty, tr, tp, o_tma, gamma, scale,
                  out, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), ks, static_cast<WsHeader*>(ws),
-                 kTimeout, ep);
+                 limit > 0 ? limit : kTimeout, skip_producer, ep);
   if (e == cudaSuccess && ks > 1) {
     const int64_t v = N % 4 == 0 ? 4 : 1, cap = static_cast<int64_t>(device_sms()) * 16, g = (M * N / v + 127) / 128;
     e = launch_pdl(v == 4 ? gemm_parts_kernel<4> : gemm_parts_kernel<1>, static_cast<unsigned>(g < cap ? g : cap), 128,

@@ -90,7 +90,7 @@ cudaError_t launch_gemm_operands(const uint8_t* packed, int fmt, int64_t rowbyte
                                  cudaStream_t st);
 cudaError_t launch_gemm_i8(const int8_t* xq, int64_t ldx, const int8_t* w, int64_t ldw, const float* gamma,
                            const float* scale, void* y, int ydt, int64_t M, int64_t N, int64_t K, const Epilogue& ep,
-                           int32_t* part, void* ws, cudaStream_t st);
+                           int32_t* part, void* ws, long long limit, int skip_producer, cudaStream_t st);
 int gemm_i8_parts(int64_t M, int64_t N, int64_t K);  // part: [this][M][N], or unused when 1
 // The product with an epilogue of up to 64 tokens, from packed weights; scratch
 // of gemm_few_bytes for the tokens' codes.
@@ -173,6 +173,8 @@ struct GradDwScratch {
 };
 cudaError_t launch_grad_dw(const uint16_t* dz, const int8_t* xq, const float* scale, const float* gamma, int64_t M,
                            int64_t N, int64_t K, float* dw, const GradDwScratch& s, void* ws, cudaStream_t st);
+// Both products on 2 KB at op with their producers switched off (the self test).
+cudaError_t launch_grad_selftest(void* op, void* ws, long long limit, cudaStream_t st);
 
 // The norms around a block's end.  Backward scratch: part [norm_grad_blocks(M, K)]
 // [4][K], gpart [norm_grad_blocks(M, K) + gate rows][K], stats [M][8] fp32.

@@ -432,12 +432,14 @@ BL_API bl_status bitlinear_residual_norm_backward(const bl_residual_norm_params 
                                                const bl_residual_norm_grads *g, void *ws, size_t ws_bytes,
                                                void *stream);
 
-/* Failure-detection self test: launches the tensor-core kernel with its data
- * producer switched off and a wait limit of about a millisecond, so that its
- * bounded waits run out; the kernel then records BL_ERR_DEVICE_TIMEOUT in the
- * workspace flag, frees what it holds and exits (no memory is read or written
- * besides the flag).  Read the result with bitlinear_device_status.  The pages
- * have no counterpart; this tests the error path of every wait.
+/* Failure-detection self test: launches the tensor-core kernels (the 2-bit GEMM,
+ * the int8 product of bitlinear_forward_epilogue, the gradient products) with
+ * their data producers switched off and a wait limit of about a millisecond, so
+ * that their bounded waits run out; each kernel then records
+ * BL_ERR_DEVICE_TIMEOUT in the workspace flag, frees what it holds and exits
+ * (nothing is written besides the flag).  Read the result with
+ * bitlinear_device_status.  The pages have no counterpart; this tests the error
+ * path of the waits.
  *   ws  at least BL_WS_HEADER_BYTES + 8192 bytes. */
 BL_API bl_status bitlinear_selftest_wait_timeout(void *ws, size_t ws_bytes, void *stream);
 
