@@ -295,7 +295,11 @@ def _calls():
         lib()
         if not os.path.exists(CALLS_PATH):
             raise RuntimeError(f"{CALLS_PATH} is missing: build it first (python -m bitlinear_b1_fwd_b200.build)")
-        from . import _calls as native
+        try:
+            from . import _calls as native
+        except ImportError as e:  # compiled for another Python or torch
+            raise RuntimeError(f"{CALLS_PATH} does not load here: build it again "
+                               f"(python -m bitlinear_b1_fwd_b200.build)") from e
         _native = native
     return _native
 

@@ -81,11 +81,25 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     return LIB
 
 
+def calls_stamp() -> str:
+    """What _calls.so is compiled for: it holds this text, and loads into nothing else."""
+    from importlib.metadata import version  # (importing torch takes seconds)
+    return f"bl_calls for {sys.implementation.cache_tag}, torch {version('torch')}"
+
+
+def calls_stale(path: str = CALLS) -> bool:
+    """Whether _calls.so is missing, older than its sources, or of another Python or torch."""
+    if _stale(path, [os.path.join(CSRC, "bl_calls.cpp"), os.path.join(INCLUDE, "bitlinear.h")]):
+        return True
+    with open(path, "rb") as f:
+        return calls_stamp().encode() + b"\0" not in f.read()
+
+
 def _build_calls(force: bool = False) -> None:
     """Compile csrc/bl_calls.cpp into _calls.so."""
-    src = os.path.join(CSRC, "bl_calls.cpp")
-    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "bitlinear.h")]):
+    if not force and not calls_stale():
         return
+    src = os.path.join(CSRC, "bl_calls.cpp")
     import sysconfig
 
     import torch
@@ -95,7 +109,8 @@ def _build_calls(force: bool = False) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBL_CALLS_STAMP="{calls_stamp()}"',
+           "-I", INCLUDE,
            *(x for i in incs for x in ("-isystem", i)), src, "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda", "-L", HERE, "-l:libbitlinear.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -353,4 +353,13 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, n
 
 }  // namespace
 
-extern "C" PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&kModule); }
+// built_for: the Python and torch this was compiled against (build.py looks for it in
+// the file)
+extern "C" PyMODINIT_FUNC PyInit__calls(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", BL_CALLS_STAMP) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
