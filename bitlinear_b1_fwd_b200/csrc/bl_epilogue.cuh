@@ -106,20 +106,14 @@ __device__ __forceinline__ void store_out(void* p, int dt, int64_t o, float v) {
     static_cast<__nv_bfloat16*>(p)[o] = __float2bfloat16_rn(v);
 }
 
-// One output of column n (of the whole matrix) at element o of y.
+// One output of column n (of the whole matrix) at element o of y (fp32 or bf16).
 __device__ __forceinline__ void epilogue_store(const Epilogue& ep, void* y, int ydt, int64_t o, int64_t n, int acc,
                                                float cf) {
-  if (ydt == BL_I32) {
-    static_cast<int32_t*>(y)[o] = acc;
-    return;
-  }
   float v = __fmul_rn(__int2float_rn(acc), cf);
-  if (ep.act >= 0) {
-    v = __fadd_rn(v, ep.bias != nullptr ? __ldcg(ep.bias + n) : 0.0f);
-    if (ep.pre != nullptr) store_out(ep.pre, ydt, o, v);
-    v = ydt == BL_BF16 ? act_apply<true>(ep.act, v) : act_apply<false>(ep.act, v);
-    if (ep.res != nullptr) v = __fadd_rn(v, load_out(ep.res, ydt, o));
-  }
+  v = __fadd_rn(v, ep.bias != nullptr ? __ldcg(ep.bias + n) : 0.0f);
+  if (ep.pre != nullptr) store_out(ep.pre, ydt, o, v);
+  v = ydt == BL_BF16 ? act_apply<true>(ep.act, v) : act_apply<false>(ep.act, v);
+  if (ep.res != nullptr) v = __fadd_rn(v, load_out(ep.res, ydt, o));
   store_out(y, ydt, o, v);
 }
 
