@@ -1078,6 +1078,44 @@ def run_profile_case(name):
         sys.exit(1)
 
 
+def run_operators():
+    """Times the listed cases of perf/operators.py: us a pass among others, three states in turn (weights and inputs
+    change from pass to pass), the median of five runs of at least 0.1 s by CUDA events.  The floor is the larger of a
+    case's bytes and operations at the measured rates (int8 products at twice the bf16 rate; dW carries two parts)."""
+    import importlib.util
+
+    import torch
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    hbm, _ = measured_peaks()
+    with open(os.path.join(ROOT, "MEASURED_PEAKS.json")) as f:
+        tflops = json.load(f)["bf16_tflops"]
+    for case in ops.listed():
+        us = {}
+        for own in (False, True):
+            ops.own = own
+            states = [ops.prepare(case, seed) for seed in range(3)]
+
+            def passes(n):
+                start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                torch.cuda.synchronize()
+                start.record()
+                for i in range(n):
+                    ops.run(states[i % 3])
+                end.record()
+                torch.cuda.synchronize()
+                return start.elapsed_time(end) / n * 1e3
+
+            passes(6)
+            n = max(6, int(1e5 / passes(6)))
+            us[own] = statistics.median(passes(n) for _ in range(5))
+        work = ops.work(case)
+        flops = work["flops"] * {"forward": 0.5, "products": 1.5}.get(case["op"], 0)  # in bf16 MACs' time
+        print(json.dumps({"case": case["name"], "floor_us": round(max(work["bytes"] / hbm * 1e-3, flops / tflops * 1e-6), 2),
+                          "plain_us": round(us[False], 1), "kernels_us": round(us[True], 2)}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -1099,9 +1137,14 @@ def main():
                     help="also time the 70B layers over M = 1..8192 and the 3B block at M = 1, 16, 128, 1024")
     ap.add_argument("--profile-case", choices=sorted(PROFILE_CASES), default=None,
                     help="run one small standalone case (for ncu captures) and exit")
+    ap.add_argument("--operators", action="store_true",
+                    help="time the listed cases of perf/operators.py, plain form and kernels, one JSON line each, and exit")
     args = ap.parse_args()
     if args.profile_case:
         run_profile_case(args.profile_case)
+        return
+    if args.operators:
+        run_operators()
         return
     wl = WORKLOADS[args.workload]
 

@@ -17,8 +17,8 @@ namespace bl {
 // results under 2^-118 may be 0.  Every
 // kernel uses the same form for the same output type.  The difference is some 15
 // and 40 instructions per output: 4096 x 3200 -> 8640 with SiLU and the kept
-// pre-activation took 123 us with the first form and 109 with the second, with
-// GELU and a residual 136 and 115.
+// pre-activation took 134 us with the first form and 127 with the second, with
+// GELU and a residual 158 and 134 (inputs changing from call to call).
 template <bool FAST>
 __device__ __forceinline__ float act_silu(float z) {
   float e, q;

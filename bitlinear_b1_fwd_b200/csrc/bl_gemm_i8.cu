@@ -20,10 +20,12 @@
 // pieces of a swizzled box of 32 tokens x 64 bytes, which one TMA tensor store
 // writes; the residual comes in, and the kept pre-activation goes out, through
 // boxes of the same kind.  4096 x 3200 -> 8640 with SiLU and the kept
-// pre-activation: 95 us (the int8 rate bounds it at 68), 110 with the operands.
-// Eight epilogue warps took 113, with spills.  Every wait is bounded: on expiry the kernel sets the
-// workspace timeout flag, drains what it issued, frees its tensor memory and
-// returns.
+// pre-activation, ternarized normal weights, inputs changing from call to call: 98
+// us (the int8 rate bounds it at 68), 124 with the pass over the operands before it;
+// equal weights, which draw less of the power cap, 114.  (With eight epilogue warps,
+// and spills, the product took 1.2 times as long.)  Every wait is bounded: on expiry
+// the kernel sets the workspace timeout flag, drains what it issued, frees its
+// tensor memory and returns.
 #include <cuda.h>
 #include <cstring>
 
