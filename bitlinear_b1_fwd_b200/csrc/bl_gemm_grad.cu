@@ -25,7 +25,7 @@
 // 1.1e-6 off in the 2-norm with runs of 64.)  Few tiles (few tokens in dx) are
 // spread over the SMs by cutting the contraction; the parts are added in order by
 // a second kernel.  4096 x 3200 x 8640: dx 166 us (1360 TFLOP/s), dW 288 us (two
-// parts: 1570 TFLOP/s), the conversions before them 20, 32 and 48 us.
+// parts: 1570 TFLOP/s), the conversions before them 20, 30 and 45 us.
 // Every wait is bounded: on expiry the kernel sets the workspace timeout flag,
 // drains what it issued, frees its tensor memory and returns.
 #include <cuda.h>
@@ -454,9 +454,9 @@ __global__ void __launch_bounds__(256)
 // ---- dW's operands ------------------------------------------------------------------
 // Two passes over dz.  Blocks of 32 column threads (8 neighbouring columns each) x
 // 8 row threads over a range of rows; the first launch also carries the conversion
-// of x_q, the other operand, in blocks of its own.  4096 x 3200 x 8640: 110 MB in 32
-// us and 214 MB in 48 us, 0.5 and 0.7 of the copy rate, waiting for their loads (20
-// cycles of it for each instruction issued; the issue slots are 30 % busy).
+// of x_q, the other operand, in blocks of its own.  4096 x 3200 x 8640: 110 MB in 30
+// us and 214 MB in 45 us, 0.6 and 0.7 of the copy rate, waiting for their loads (20
+// cycles of it for each instruction issued; the issue slots are 31 % busy).
 constexpr int kGcCols = 256, kGcRows = 8, kGcUnroll = 4;
 
 // dz[m, n0 .. n0 + 7] (zeros past N)
