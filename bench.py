@@ -1088,9 +1088,7 @@ def run_operators():
     spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
-    hbm, _ = measured_peaks()
-    with open(os.path.join(ROOT, "MEASURED_PEAKS.json")) as f:
-        tflops = json.load(f)["bf16_tflops"]
+    hbm, tflops = measured_peaks()[0], measured_int8_peak()[0] / INT8_PER_BF16
     for case in ops.listed():
         us = {}
         for own in (False, True):

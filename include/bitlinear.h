@@ -352,8 +352,8 @@ BL_API bl_status bitlinear_epilogue_backward(const void *dy, int dydt, const voi
  *       power of two per output row n so that the row's largest entry v_n is
  *       at 2^13, times the exact x_q: 22 bits of an entry, but no less than
  *       2^-38 v_n (an entry far below the row's largest loses bits, and from
- *       2^-39 v_n on is 0).  A row with an infinity, a NaN or a dz s_m beyond
- *       fp32 gives a row of NaN.
+ *       2^-39 v_n on is 0), or 2^-151 for rows below 2^-113.  A row with an
+ *       infinity, a NaN or a dz s_m beyond fp32 gives a row of NaN.
  * Both add runs of contracted elements (512 for dx, 256 for dW) on the tensor
  * core in fp32 and the runs in fp32 registers in order: the same bits on every
  * call (dx of up to 32 tokens: runs of the same length on another kernel).  The
